@@ -69,7 +69,8 @@ extern "C" {
 #define MACAQ_ERR_GROUP_LIST_INVALID (-10)/* (device) group_list breaks the rules */
 #define MACAQ_ERR_WORKSPACE (-11)         /* workspace missing or too small */
 #define MACAQ_ERR_BAD_D (-12)             /* D has a zero or non-finite entry */
-#define MACAQ_ERR_ACT_TYPE (-13)          /* act_type not 0, 1, 2, 4 or 5 */
+#define MACAQ_ERR_ACT_TYPE (-13)          /* act_type not one the call takes */
+#define MACAQ_ERR_OPTION (-14)            /* an element type, score or factor outside what the call takes */
 
 /* Name of a status code (static string). */
 const char *macaq_status_string(int status);
@@ -261,6 +262,103 @@ int macaq_grouped_mm_plain(const uint16_t *x_dev, const uint8_t *Wq_dev, const u
                            const int64_t *group_list_dev, int group_list_type, int64_t E, uint16_t *y_dev,
                            int64_t M, int64_t N, int64_t K, void *workspace_dev, size_t workspace_bytes,
                            int32_t *status_dev, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Around the linear: norms, routing, the mixture-of-experts layer     */
+/* ------------------------------------------------------------------ */
+
+/* Element types of arguments that may be either. */
+#define MACAQ_BF16 0
+#define MACAQ_FP32 1
+
+/* What stands between two blocks of a model: the norm after a block, its gate
+ * and residual scale, the residual sum, and the norm before the next block, in
+ * one pass over the rows:
+ *     p  = y                      or (w_post given)
+ *          y * rsqrt(mean(y^2) + eps) * (weight_offset + w_post)
+ *     h' = round_T(h + scale * gate * p)            T = bf16 or fp32 (h_type)
+ *     n  = RNE_bf16(h' * rsqrt(mean(h'^2) + eps) * (weight_offset + w_pre))
+ * Means over the C elements of a row; sums and products in FP32.  h' is rounded
+ * once, to the type it is stored in, and the second norm reads that value: n is
+ * bf16, the activation type of the linears.
+ *   h_dev       [M, C] of h_type (MACAQ_BF16 / MACAQ_FP32), the residual stream;
+ *   y_dev       bf16 [M, C], the block's output, or NULL (then w_post, gate and
+ *               h_out must be NULL too, and n is the norm of h);
+ *   w_post_dev  fp32 [C] or NULL: y is added as it is;
+ *   gate_dev    [ceil(M / rows_per_gate), C] of gate_type or NULL: row m takes
+ *               gate row m / rows_per_gate (1: a gate per token; a sequence's
+ *               length: one per sequence; M: one learned scale per channel);
+ *   w_pre_dev   fp32 [C], or NULL together with n_out (no second norm);
+ *   h_out_dev   [M, C] of h_type; may be h_dev itself (in place), may not
+ *               overlap any other argument;  n_out_dev bf16 [M, C], may not
+ *               overlap any argument.
+ * scale, eps (>= 0) and weight_offset must be finite, else MACAQ_ERR_OPTION.
+ * Shapes: 0 <= M <= 2^31 - 1; 16 <= C <= 65536 with C % 16 == 0. */
+int macaq_block_norm(const void *h_dev, int h_type, const uint16_t *y_dev, const float *w_post_dev,
+                     const void *gate_dev, int gate_type, int64_t rows_per_gate, const float *w_pre_dev, float scale,
+                     float eps, float weight_offset, void *h_out_dev, uint16_t *n_out_dev, int64_t M, int64_t C,
+                     void *stream);
+
+/* Scores that turn router logits into weights. */
+#define MACAQ_SCORE_SOFTMAX 0 /* over all E logits of a token */
+#define MACAQ_SCORE_SIGMOID 1 /* of each logit by itself */
+
+/* Routing: for each token the k experts of the largest logits (in falling order,
+ * equal logits by the lowest index, a NaN as -infinity) and their weights
+ *     w_j = scale * score(l_j)      or (renorm != 0) scale * score(l_j) / sum over the k
+ * in FP32, and, sorted by expert, which rows the grouped linear would take:
+ *   logits_dev   [T, E] of logits_type;
+ *   ids_dev      int32 [T, k];  weights_dev fp32 [T, k];
+ *   counts_dev   int64 [E], the choices of each expert: a group_list of type 1
+ *                over T k rows;
+ *   order_dev    int32 [T k]: row r of the sorted rows belongs to choice
+ *                order[r] = t k + j (token order[r] / k), by expert, within an
+ *                expert by token.  counts and order may both be NULL.
+ * A logit of -infinity has weight zero, also in a token that has no other (its
+ * ids are then the lowest experts); a sigmoid below 2^-126 is zero.  A NaN logit
+ * makes a weight NaN where it is chosen or enters its sum.
+ * Shapes: 0 <= T, T k <= 2^31 - 1; 1 <= E <= 1024 (MACAQ_ERR_TOO_MANY_GROUPS);
+ * 1 <= k <= min(E, 32).  The workspace (macaq_route_workspace_bytes, 0 for a few
+ * tokens) is used when counts is given; nothing in it has to start at zero. */
+size_t macaq_route_workspace_bytes(int64_t T, int64_t E);
+int macaq_moe_route(const void *logits_dev, int logits_type, int64_t T, int64_t E, int64_t k, int score, int renorm,
+                    float scale, int32_t *ids_dev, float *weights_dev, int64_t *counts_dev, int32_t *order_dev,
+                    void *workspace_dev, size_t workspace_bytes, void *stream);
+
+/* macaq_prepare_weights for the first linear of a gated layer: W_dev fp32
+ * [E, 2 I, K], per expert I gate rows followed by I up rows.  The images hold
+ * them interleaved (row 2 c: gate row c, row 2 c + 1: up row c), so both halves
+ * of a channel come out of one tile; sizes are macaq_weight_*_bytes(E, 2 I, K).
+ * Same checks and synchronisation as macaq_prepare_weights. */
+int macaq_prepare_gate_up(const float *W_dev, const float *D_dev, int64_t E, int64_t I, int64_t K, uint8_t *Wq_dev,
+                          uint8_t *Ws_dev, void *stream);
+
+/* A whole mixture-of-experts layer for a few tokens, from the router's logits to
+ * the sum of the experts, in two kernels.  With the ids and weights that
+ * macaq_moe_route gives for these logits, for e = ids[t, j]:
+ *     (g, u) = 2^-5 Q(H(x[t] / D_up_e)) . Wup_e^T          (FP32)
+ *     a      = RNE_bf16(act(g) * u)
+ *     y[t]   = RNE_bf16( sum_j w[t, j] * 2^-5 Q(H(a / D_down_e)) . Wdown_e^T )
+ * each product the MACAQ linear of this library with FP32 accumulation; the sum
+ * over the experts is FP32 in a fixed order.  A choice of weight zero is left
+ * out: its expert is not read, and a token whose logits are all -infinity (a
+ * padded row) gives zeros.
+ *   x_dev bf16 [T, H];  logits_dev [T, E] of logits_type;
+ *   D_up_dev fp32 [E, H]; Wq_up/Ws_up from macaq_prepare_gate_up(E, I, H);
+ *   D_down_dev fp32 [E, I]; Wq_down/Ws_down from macaq_prepare_weights(E, H, I);
+ *   act_type 5 (SILU) or 2 (GELU_TANH), else MACAQ_ERR_ACT_TYPE;
+ *   y_dev bf16 [T, H]; workspace: macaq_moe_workspace_bytes(T, k, I) bytes
+ *   (the activations a); nothing in it has to start at zero, and calls that
+ *   share it must not run concurrently.
+ *   The activation is evaluated with an FP32 exponential and division.
+ * Shapes: 0 <= T <= 128; 1 <= E <= 512; 1 <= k <= min(E, 16); H and I multiples
+ * of 256 in [256, 8192]. */
+size_t macaq_moe_workspace_bytes(int64_t T, int64_t k, int64_t I);
+int macaq_moe_mm(const uint16_t *x_dev, const void *logits_dev, int logits_type, const float *D_up_dev,
+                 const uint8_t *Wq_up_dev, const uint8_t *Ws_up_dev, const float *D_down_dev,
+                 const uint8_t *Wq_down_dev, const uint8_t *Ws_down_dev, int64_t T, int64_t E, int64_t k, int64_t H,
+                 int64_t I, int score, int renorm, float scale, int act_type, uint16_t *y_dev, void *workspace_dev,
+                 size_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* Test and ablation entry points (not the product's hot path)         */

@@ -35,11 +35,14 @@ STATUS = {
     -4: "MACAQ_ERR_ARCH", -5: "MACAQ_ERR_ALIAS", -6: "MACAQ_ERR_TOO_MANY_GROUPS",
     -7: "MACAQ_ERR_GROUP_LIST_TYPE", -8: "MACAQ_ERR_CUDA", -9: "MACAQ_ERR_DEVICE_TIMEOUT",
     -10: "MACAQ_ERR_GROUP_LIST_INVALID", -11: "MACAQ_ERR_WORKSPACE", -12: "MACAQ_ERR_BAD_D",
-    -13: "MACAQ_ERR_ACT_TYPE",
+    -13: "MACAQ_ERR_ACT_TYPE", -14: "MACAQ_ERR_OPTION",
 }
 
 # npu_grouped_matmul act_type values accepted by the _ex calls (3 is not supported)
 ACT_NONE, ACT_RELU, ACT_GELU_TANH, ACT_FAST_GELU, ACT_SILU = 0, 1, 2, 4, 5
+
+# scores of moe_route and moe_mm
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 
 class MacaqError(RuntimeError):
@@ -106,6 +109,16 @@ _SIG = {
                                              _I64, _I64, _P, ctypes.c_size_t, _P, _P]),
     "macaq_dense_mm_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_float, _P, _I64, _I64, _I64,
                                           _P, ctypes.c_size_t, _P, _P]),
+    "macaq_block_norm": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _I64, _P, ctypes.c_float,
+                                        ctypes.c_float, ctypes.c_float, _P, _P, _I64, _I64, _P]),
+    "macaq_route_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "macaq_moe_route": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.c_float,
+                                       _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "macaq_prepare_gate_up": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "macaq_moe_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "macaq_moe_mm": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64,
+                                    ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int, _P, _P,
+                                    ctypes.c_size_t, _P, _P]),
     "macaq_grouped_mm_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, _I64, _P, ctypes.c_int,
                                             ctypes.c_float, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P, _P]),
 }
@@ -622,3 +635,203 @@ def mx_encode_blocks(v: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.
     _check(lib().macaq_mx_encode_blocks(_ptr(v), _ptr(codes), _ptr(scales), n, _stream_ptr(stream)),
            "macaq_mx_encode_blocks")
     return codes, scales
+
+
+# ---------------------------------------------------------------------------
+# around the linear: norms, routing, the mixture-of-experts layer
+# ---------------------------------------------------------------------------
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # MACAQ_BF16, MACAQ_FP32
+
+
+def _element_type(t: torch.Tensor, name: str) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return code
+
+
+def _shape(t, name: str, dtype, shape: tuple):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Place:
+    """The device and stream of a call: the first tensor's device (every other
+    tensor must be on it, contiguous), made current for the launch, and the given
+    stream or that device's current one.  Allocations are made on that stream."""
+
+    __slots__ = ("device", "stream", "_contexts")
+
+    def __init__(self, stream, *ts):
+        first = ts[0]
+        device = first.device
+        for t in ts:
+            if t is not None and (not t.is_cuda or not t.is_contiguous() or t.device != device):
+                raise ValueError("expected contiguous CUDA tensors on one device")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.device, self.stream, self._contexts = device, stream, ()
+
+    def __enter__(self):
+        if self.stream is not None:
+            self._contexts = (torch.cuda.stream(self.stream),)  # makes its device current too
+        elif torch.cuda.current_device() != self.device.index:
+            self._contexts = (torch.cuda.device(self.device),)
+        for c in self._contexts:
+            c.__enter__()
+        return self
+
+    def __exit__(self, *e):
+        for c in self._contexts:
+            c.__exit__(*e)
+
+    def raw(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def scratch(self, nbytes: int, given: torch.Tensor | None):
+        """Workspace of a call.  A captured call gets memory of its own from the graph's
+        pool: two graphs never share it, and the kept buffer may be regrown later."""
+        if nbytes > 0 and given is None and torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return workspace(nbytes, self.device, self.stream, given)
+
+
+def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, rows_per_gate: int | None = None,
+               w_pre: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0,
+               out_h: torch.Tensor | None = None, out_n: torch.Tensor | None = None,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """What stands between two blocks, in one kernel: h' = h + scale * gate * post(y) and
+    n = pre(h'), RMS norms with weights (weight_offset + w); returns (h', n).
+
+    h bf16 or fp32 [M, C] (h' keeps its type; out_h may be h itself); y bf16 [M, C] or None
+    (h' is h); w_post, w_pre fp32 [C] (None: no norm there; without w_pre n is None); gate
+    bf16 or fp32, [C] for one gate of all rows or [G, C] where row m takes gate row
+    m // rows_per_gate (default 1: one per row)."""
+    h_type = _element_type(h, "h")
+    if h.dim() != 2:
+        raise ValueError(f"h must have 2 dimensions, got shape {tuple(h.shape)}")
+    M, C = h.shape
+    _shape(y, "y", torch.bfloat16, (M, C))
+    _shape(w_post, "w_post", torch.float32, (C,))
+    _shape(w_pre, "w_pre", torch.float32, (C,))
+    _shape(out_h, "out_h", h.dtype, (M, C))
+    _shape(out_n, "out_n", torch.bfloat16, (M, C))
+    gate_type, per = 0, 1
+    if gate is not None:
+        gate_type = _element_type(gate, "gate")
+        if gate.dim() == 1:
+            per, want = max(1, M), (C,)
+            if rows_per_gate not in (None, per):
+                raise ValueError("a gate of one dimension is shared by all rows: rows_per_gate does not apply")
+        else:
+            per = 1 if rows_per_gate is None else int(rows_per_gate)
+            if per < 1:
+                raise ValueError(f"rows_per_gate must be at least 1, got {rows_per_gate}")
+            want = (-(-M // per), C)
+        _shape(gate, "gate", gate.dtype, want)
+    if y is None and (w_post is not None or gate is not None or out_h is not None):
+        raise ValueError("w_post, gate and out_h go with y")
+    if w_pre is None and out_n is not None:
+        raise ValueError("out_n goes with w_pre")
+    with _Place(stream, h, y, w_post, gate, w_pre, out_h, out_n) as at:
+        h_out = out_h if y is None or out_h is not None else torch.empty_like(h)
+        n = out_n if w_pre is None or out_n is not None else torch.empty((M, C), dtype=torch.bfloat16, device=h.device)
+        _check(lib().macaq_block_norm(_at(h), h_type, _at(y), _at(w_post), _at(gate), gate_type, per, _at(w_pre),
+                                      scale, eps, weight_offset, _at(h_out), _at(n), M, C, at.raw()),
+               "macaq_block_norm")
+    return (h if y is None else h_out), n
+
+
+def moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
+              sort: bool = True, stream=None, ws: torch.Tensor | None = None):
+    """Routing from logits bf16 or fp32 [T, E]: (ids int32 [T, k], weights fp32 [T, k],
+    counts int64 [E], order int32 [T k]); row r of the rows sorted by expert belongs to
+    token order[r] // k, and counts is grouped_mm's group_list of type 1 for them.
+    counts and order are None without sort."""
+    logits_type = _element_type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have 2 dimensions, got shape {tuple(logits.shape)}")
+    T, E = logits.shape
+    if not 1 <= k <= min(E, 32):
+        raise ValueError(f"k must be between 1 and min(E, 32) = {min(E, 32)}, got {k}")
+    L = lib()
+    with _Place(stream, logits, ws) as at:
+        dev = logits.device
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        counts = order = None
+        need = 0
+        if sort:
+            counts = torch.empty(E, dtype=torch.int64, device=dev)
+            order = torch.empty(T * k, dtype=torch.int32, device=dev)
+            need = L.macaq_route_workspace_bytes(T, E)
+        ws = at.scratch(need, ws)
+        _check(L.macaq_moe_route(_at(logits), logits_type, T, E, k, score, bool(renorm), scale, _at(ids), _at(weights),
+                                 _at(counts), _at(order) if T else None, _at(ws), _nbytes(ws), at.raw()),
+               "macaq_moe_route")
+    return ids, weights, counts, order
+
+
+def prepare_gate_up(W: torch.Tensor, D: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Offline: the first linear of a gated layer, W fp32 [2 I, K] or [E, 2 I, K] (I gate rows,
+    then I up rows), D fp32 [K] or [E, K] -> the (Wq, Ws) tile images moe_mm takes."""
+    if W.dim() == 2:
+        W = W.unsqueeze(0)
+    if D.dim() == 1:
+        D = D.unsqueeze(0)
+    _arg(W, "W", torch.float32, ndim=3)
+    E, N, K = W.shape
+    if N % 2:
+        raise ValueError(f"W holds as many gate rows as up rows, got {N} rows")
+    _shape(D, "D", torch.float32, (E, K))
+    qb, sb = weight_bytes(E, N, K)
+    if qb == 0:
+        raise MacaqError(-3, "prepare_gate_up")
+    with _Place(stream, W, D) as at:
+        Wq = torch.empty(qb, dtype=torch.uint8, device=W.device)
+        Ws = torch.empty(sb, dtype=torch.uint8, device=W.device)
+        _check(lib().macaq_prepare_gate_up(_at(W), _at(D), E, N // 2, K, _at(Wq), _at(Ws), at.raw()),
+               "macaq_prepare_gate_up")
+    return Wq, Ws
+
+
+def moe_workspace_bytes(T: int, k: int, inner: int) -> int:
+    return int(lib().macaq_moe_workspace_bytes(T, k, inner))
+
+
+def moe_mm(x: torch.Tensor, logits: torch.Tensor, D_up: torch.Tensor, Wq_up: torch.Tensor, Ws_up: torch.Tensor,
+           D_down: torch.Tensor, Wq_down: torch.Tensor, Ws_down: torch.Tensor, inner: int, k: int,
+           score: int = SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0, act_type: int = ACT_SILU,
+           out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None,
+           ws: torch.Tensor | None = None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for T <= 128 tokens: y bf16 [T, H] from x bf16 [T, H]
+    and the router's logits bf16 or fp32 [T, E], the experts chosen and weighted as by
+    moe_route.  D_up fp32 [E, H] with the images of prepare_gate_up, D_down fp32 [E, inner]
+    with those of prepare_weights ([E, H, inner])."""
+    _arg(x, "x", torch.bfloat16, ndim=2)
+    logits_type = _element_type(logits, "logits")
+    T, H = x.shape
+    if logits.dim() != 2 or logits.shape[0] != T:
+        raise ValueError(f"logits must be [{T}, E], got shape {tuple(logits.shape)}")
+    E = logits.shape[1]
+    _shape(D_up, "D_up", torch.float32, (E, H))
+    _shape(D_down, "D_down", torch.float32, (E, inner))
+    _shape(out, "out", torch.bfloat16, (T, H))
+    _arg(status, "status", torch.int32, min_numel=1)
+    L = lib()
+    for q, s, name, N, K in ((Wq_up, Ws_up, "up", 2 * inner, H), (Wq_down, Ws_down, "down", H, inner)):
+        _arg(q, "Wq_" + name, torch.uint8, min_numel=L.macaq_weight_code_bytes(E, N, K))
+        _arg(s, "Ws_" + name, torch.uint8, min_numel=L.macaq_weight_scale_bytes(E, N, K))
+    with _Place(stream, x, logits, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, out, status, ws) as at:
+        y = torch.empty_like(x) if out is None else out
+        ws = at.scratch(L.macaq_moe_workspace_bytes(T, k, inner), ws)
+        _check(L.macaq_moe_mm(_at(x), _at(logits), logits_type, _at(D_up), _at(Wq_up), _at(Ws_up), _at(D_down),
+                              _at(Wq_down), _at(Ws_down), T, E, k, H, inner, score, bool(renorm), scale, act_type,
+                              _at(y), _at(ws), _nbytes(ws), _at(status), at.raw()), "macaq_moe_mm")
+    return y

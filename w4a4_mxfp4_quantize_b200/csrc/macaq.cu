@@ -33,6 +33,10 @@
 //                         the swizzled B tile straight into shared memory;
 //                         optional split-K across a thread-block cluster, partial
 //                         sums reduced through distributed shared memory
+//   block_norm_kernel     the norms around a block with its gate and residual (norm.cuh)
+//   route_choose_kernel, route_place_kernel
+//                         top-k of router logits, rows sorted by expert (route.cuh)
+//   moe_kernel            mixture-of-experts layer for a few tokens (moe.cuh)
 //   quant_canonical_kernel, export_tiles_kernel, mx_encode_kernel: tests only
 #include <cuda_runtime.h>
 
@@ -45,7 +49,9 @@
 
 #include "macaq.h"
 #include "mx.cuh"
+#include "norm.cuh"
 #include "ptx.cuh"
+#include "route.cuh"
 
 namespace macaq {
 
@@ -149,7 +155,9 @@ constexpr int kActImageBytes = kTileCodeBytes + kTileSfBytes;  // 17408
 // CTA = 32 rows x one 256-wide K tile (256 threads, one 32-block each).
 // kPlain: plain MXFP4 of W itself (no D, no Hadamard; D is not read).
 // kTrans: W is stored transposed, [E, K, N] (element (n, k) at (e K + k) N + n).
-template <bool kPlain, bool kTrans = false>
+// kPairs: W holds N / 2 gate rows, then N / 2 up rows; image row 2 c takes gate row c,
+// image row 2 c + 1 up row c.
+template <bool kPlain, bool kTrans = false, bool kPairs = false>
 __global__ void __launch_bounds__(256) prep_weights_kernel(const float* __restrict__ W, const float* __restrict__ D,
                                                            uint8_t* __restrict__ Wq, uint8_t* __restrict__ Ws,
                                                            int N, int K, int NT) {
@@ -171,7 +179,8 @@ __global__ void __launch_bounds__(256) prep_weights_kernel(const float* __restri
 #pragma unroll
       for (int i = 0; i < 32; ++i) wv[i] = __ldg(wp + static_cast<int64_t>(i) * N);
     } else {
-      const float4* wp = reinterpret_cast<const float4*>(W + (static_cast<int64_t>(e) * N + n) * K + k0);
+      const int src = kPairs ? (n >> 1) + (n & 1) * (N >> 1) : n;
+      const float4* wp = reinterpret_cast<const float4*>(W + (static_cast<int64_t>(e) * N + src) * K + k0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float4 a = __ldg(wp + i);
@@ -1651,6 +1660,8 @@ __global__ void __launch_bounds__(fused::kThreads, 1) fused_small_kernel(const _
 
 }  // namespace macaq
 
+#include "moe.cuh"
+
 // ============================================================================
 // Host side: argument checks, variant choice, launches
 // ============================================================================
@@ -1706,6 +1717,8 @@ int current_device(int& dev, int& sms) {
     ok = ok && fused_attrs<16>() && fused_attrs<32>() && fused_attrs<64>() && fused_attrs<128>();
     ok = ok && cudaFuncSetAttribute(quant_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQuantSmem) ==
                    cudaSuccess;
+    ok = ok && cudaFuncSetAttribute(moe_kernel<false>, a, gs) == cudaSuccess &&
+         cudaFuncSetAttribute(moe_kernel<true>, a, gs) == cudaSuccess;
     if (!ok) return MACAQ_ERR_CUDA;
     s.attrs_set = true;
   }
@@ -2027,6 +2040,7 @@ const char* macaq_status_string(int s) {
     case MACAQ_ERR_WORKSPACE: return "MACAQ_ERR_WORKSPACE";
     case MACAQ_ERR_BAD_D: return "MACAQ_ERR_BAD_D";
     case MACAQ_ERR_ACT_TYPE: return "MACAQ_ERR_ACT_TYPE";
+    case MACAQ_ERR_OPTION: return "MACAQ_ERR_OPTION";
     default: return "MACAQ_ERR_UNKNOWN";
   }
 }
@@ -2044,7 +2058,7 @@ size_t macaq_weight_scale_bytes(int64_t E, int64_t N, int64_t K) {
 }
 
 static int prepare_impl(const float* W, const float* D, int64_t E, int64_t N, int64_t K, uint8_t* Wq, uint8_t* Ws,
-                        void* stream, bool trans);
+                        void* stream, bool trans, bool pairs = false);
 
 int macaq_prepare_weights(const float* W, const float* D, int64_t E, int64_t N, int64_t K, uint8_t* Wq, uint8_t* Ws,
                           void* stream) {
@@ -2056,8 +2070,14 @@ int macaq_prepare_weights_transposed(const float* W_kn, const float* D, int64_t 
   return prepare_impl(W_kn, D, E, N, K, Wq, Ws, stream, true);
 }
 
+int macaq_prepare_gate_up(const float* W, const float* D, int64_t E, int64_t I, int64_t K, uint8_t* Wq, uint8_t* Ws,
+                          void* stream) {
+  if (I < 1 || I > 32768) return MACAQ_ERR_SHAPE;
+  return prepare_impl(W, D, E, 2 * I, K, Wq, Ws, stream, false, true);
+}
+
 static int prepare_impl(const float* W, const float* D, int64_t E, int64_t N, int64_t K, uint8_t* Wq, uint8_t* Ws,
-                        void* stream, bool trans) {
+                        void* stream, bool trans, bool pairs) {
   if (E < 1 || E > kMaxGroups) return MACAQ_ERR_TOO_MANY_GROUPS;
   if (!valid_nk(N, K)) return MACAQ_ERR_SHAPE;
   if (!W || !D || !Wq || !Ws) return MACAQ_ERR_NULL;
@@ -2080,7 +2100,9 @@ static int prepare_impl(const float* W, const float* D, int64_t E, int64_t N, in
     if (!(d != 0.0f) || !std::isfinite(d)) return MACAQ_ERR_BAD_D;
   const int NTP = static_cast<int>(pad256(N) / 128);  // images per expert, pairs complete
   dim3 grid(static_cast<unsigned>(E * NTP * 4), static_cast<unsigned>(K / 256));
-  if (trans)
+  if (pairs)
+    prep_weights_kernel<false, false, true><<<grid, 256, 0, s>>>(W, D, Wq, Ws, static_cast<int>(N), static_cast<int>(K), NTP);
+  else if (trans)
     prep_weights_kernel<false, true><<<grid, 256, 0, s>>>(W, D, Wq, Ws, static_cast<int>(N), static_cast<int>(K), NTP);
   else
     prep_weights_kernel<false, false><<<grid, 256, 0, s>>>(W, D, Wq, Ws, static_cast<int>(N), static_cast<int>(K), NTP);
@@ -2529,6 +2551,236 @@ int macaq_unfused_dense_mm(const uint16_t* x, const float* D, const uint8_t* Wq,
   if (st != MACAQ_OK) return st;
   return run_dense_two_kernel(x, D, Wq, Ws, y, M, N, K, static_cast<uint8_t*>(workspace), status,
                               static_cast<cudaStream_t>(stream), sms, false);
+}
+
+// ---- norms around a block ----
+static int norm_launch(const NormParams& p, int sms, cudaStream_t st) {
+  using Kernel = void (*)(NormParams);
+  const int vecs = p.C / 8;
+  const bool f32 = p.h_f32 != 0;
+  if (vecs > 2048) {  // more than 16384 columns do not fit a CTA's registers
+    const Kernel k = f32 ? block_norm_wide_kernel<true> : block_norm_wide_kernel<false>;
+    const int grid = std::min(p.M, 2 * sms);
+    return launch_ex(k, dim3(grid), dim3(1024), 0, st, true, 1, p) == cudaSuccess ? MACAQ_OK : MACAQ_ERR_CUDA;
+  }
+  // A warp per row up to 1024 columns where there are rows enough to fill the device,
+  // else a CTA per row with one vector (four above 8192 columns) per thread.
+  Kernel k;
+  int threads, rows_per_cta = 1;
+  if (vecs <= 128 && p.M >= 8 * sms) {
+    const int v = vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4;
+    k = v == 1 ? (f32 ? block_norm_kernel<true, 1, true> : block_norm_kernel<true, 1, false>)
+      : v == 2 ? (f32 ? block_norm_kernel<true, 2, true> : block_norm_kernel<true, 2, false>)
+               : (f32 ? block_norm_kernel<true, 4, true> : block_norm_kernel<true, 4, false>);
+    threads = 256;
+    rows_per_cta = 8;
+  } else {
+    const int v = vecs <= 1024 ? 1 : 4;
+    k = v == 1 ? (f32 ? block_norm_kernel<false, 1, true> : block_norm_kernel<false, 1, false>)
+               : (f32 ? block_norm_kernel<false, 4, true> : block_norm_kernel<false, 4, false>);
+    threads = (ceil_div(vecs, v) + 31) / 32 * 32;
+  }
+  const int per_sm = std::max(1, 2048 / threads);
+  const int grid = std::min(ceil_div(p.M, rows_per_cta), per_sm * sms);
+  return launch_ex(k, dim3(grid), dim3(threads), 0, st, true, 1, p) == cudaSuccess ? MACAQ_OK : MACAQ_ERR_CUDA;
+}
+
+static bool element_type(int t) { return t == MACAQ_BF16 || t == MACAQ_FP32; }
+static size_t element_bytes(int t) { return t == MACAQ_FP32 ? 4 : 2; }
+
+int macaq_block_norm(const void* h, int h_type, const uint16_t* y, const float* w_post, const void* gate,
+                     int gate_type, int64_t rows_per_gate, const float* w_pre, float scale, float eps,
+                     float weight_offset, void* h_out, uint16_t* n_out, int64_t M, int64_t C, void* stream) {
+  if (M < 0 || M > INT32_MAX || C < 16 || C > 65536 || C % 16 != 0) return MACAQ_ERR_SHAPE;
+  if (!element_type(h_type) || (gate != nullptr && !element_type(gate_type)) || !std::isfinite(scale) ||
+      !(std::isfinite(eps) && eps >= 0.0f) || !std::isfinite(weight_offset))
+    return MACAQ_ERR_OPTION;
+  if (gate != nullptr && rows_per_gate < 1) return MACAQ_ERR_SHAPE;
+  if (M == 0) return MACAQ_OK;
+  // without a branch there is nothing to add, gate or store; without a second norm there is no n
+  if (!h || (y != nullptr) != (h_out != nullptr) || (w_pre != nullptr) != (n_out != nullptr) || (!y && !w_pre) ||
+      (!y && (w_post != nullptr || gate != nullptr)))
+    return MACAQ_ERR_NULL;
+  const size_t hb = static_cast<size_t>(M) * C * element_bytes(h_type), yb = static_cast<size_t>(M) * C * 2;
+  const int64_t gates = gate != nullptr ? (M + rows_per_gate - 1) / rows_per_gate : 0;
+  const size_t gb = static_cast<size_t>(gates) * C * element_bytes(gate_type), wb = static_cast<size_t>(C) * 4;
+  const struct { const void* p; size_t n; } in[] = {{h, hb}, {y, yb}, {w_post, wb}, {gate, gb}, {w_pre, wb}};
+  for (const auto& i : in)
+    if (!aligned16(i.p)) return MACAQ_ERR_ALIGN;
+  if (!aligned16(h_out) || !aligned16(n_out)) return MACAQ_ERR_ALIGN;
+  for (const auto& i : in) {
+    if (i.p == nullptr) continue;
+    if (h_out != nullptr && !(i.p == h && h_out == h) && overlaps(h_out, hb, i.p, i.n)) return MACAQ_ERR_ALIAS;
+    if (n_out != nullptr && overlaps(n_out, yb, i.p, i.n)) return MACAQ_ERR_ALIAS;
+  }
+  if (h_out != nullptr && n_out != nullptr && overlaps(h_out, hb, n_out, yb)) return MACAQ_ERR_ALIAS;
+  int dev, sms;
+  const int st = current_device(dev, sms);
+  if (st != MACAQ_OK) return st;
+  NormParams p{};
+  p.h = h; p.y = y; p.w_post = w_post; p.gate = gate; p.w_pre = w_pre; p.h_out = h_out; p.n_out = n_out;
+  p.M = static_cast<int>(M); p.C = static_cast<int>(C);
+  p.rows_per_gate = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, rows_per_gate), INT32_MAX));
+  p.h_f32 = h_type == MACAQ_FP32 ? 1 : 0;
+  p.gate_f32 = gate_type == MACAQ_FP32 ? 1 : 0;
+  p.scale = scale; p.eps = eps; p.offset = weight_offset;
+  return norm_launch(p, sms, static_cast<cudaStream_t>(stream));
+}
+
+// ---- routing ----
+static int check_rule(int logits_type, int64_t E, int64_t k, int64_t max_e, int64_t max_k, int score, float scale) {
+  if (E < 1 || E > max_e) return MACAQ_ERR_TOO_MANY_GROUPS;
+  if (k < 1 || k > E || k > max_k) return MACAQ_ERR_SHAPE;
+  if (!element_type(logits_type) || (score != MACAQ_SCORE_SOFTMAX && score != MACAQ_SCORE_SIGMOID) ||
+      !std::isfinite(scale))
+    return MACAQ_ERR_OPTION;
+  return MACAQ_OK;
+}
+static RouteRule route_rule(const void* logits, int logits_type, int64_t E, int64_t k, int score, int renorm,
+                            float scale) {
+  RouteRule r{};
+  r.logits = logits;
+  r.logits_f32 = logits_type == MACAQ_FP32 ? 1 : 0;
+  r.E = static_cast<int>(E); r.k = static_cast<int>(k);
+  r.sigmoid = score == MACAQ_SCORE_SIGMOID ? 1 : 0;
+  r.renorm = renorm != 0 ? 1 : 0;
+  r.scale = scale;
+  return r;
+}
+// CTAs of the routing kernels: one up to 4 runs of tokens (it needs no second kernel),
+// then one per run up to kRouteCtas.
+static int route_ctas(int64_t T) {
+  const int64_t runs = (T + kRouteRun - 1) / kRouteRun;
+  return runs <= 1 ? 1 : static_cast<int>(std::min<int64_t>(runs, kRouteCtas));
+}
+
+size_t macaq_route_workspace_bytes(int64_t T, int64_t E) {
+  if (T <= 0 || T > INT32_MAX || E < 1 || E > kRouteMaxE) return 0;
+  const int ctas = route_ctas(T);
+  return ctas > 1 ? static_cast<size_t>(ctas) * E * 4 : 0;
+}
+
+int macaq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t k, int score, int renorm,
+                    float scale, int32_t* ids, float* weights, int64_t* counts, int32_t* order, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int st = check_rule(logits_type, E, k, kRouteMaxE, kMaxChoices, score, scale);
+  if (st != MACAQ_OK) return st;
+  if (T < 0 || T > INT32_MAX || T * k > INT32_MAX) return MACAQ_ERR_SHAPE;
+  if ((counts != nullptr) != (order != nullptr) && T > 0) return MACAQ_ERR_NULL;
+  if (T > 0 && (!logits || !ids || !weights)) return MACAQ_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(counts) || !aligned16(order))
+    return MACAQ_ERR_ALIGN;
+  const size_t lb = static_cast<size_t>(T) * E * element_bytes(logits_type), nb = static_cast<size_t>(T) * k * 4;
+  const size_t need = counts != nullptr ? macaq_route_workspace_bytes(T, E) : 0;
+  const struct { const void* p; size_t n; } t[] = {{logits, lb}, {ids, nb}, {weights, nb},
+      {counts, counts ? static_cast<size_t>(E) * 8 : 0}, {order, order ? nb : 0}, {need ? workspace : nullptr, need}};
+  for (int i = 0; i < 6; ++i)
+    for (int j = std::max(1, i + 1); j < 6; ++j)
+      if (t[i].p != nullptr && t[j].p != nullptr && overlaps(t[i].p, t[i].n, t[j].p, t[j].n)) return MACAQ_ERR_ALIAS;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return MACAQ_ERR_WORKSPACE;
+  if (T == 0 && counts == nullptr) return MACAQ_OK;
+  int dev, sms;
+  st = current_device(dev, sms);
+  if (st != MACAQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cudaMemsetAsync(counts, 0, static_cast<size_t>(E) * 8, s) == cudaSuccess ? MACAQ_OK : MACAQ_ERR_CUDA;
+  RouteParams p{};
+  p.rule = route_rule(logits, logits_type, E, k, score, renorm, scale);
+  p.T = T;
+  const int ctas = route_ctas(T);
+  p.per_cta = ceil_div(T, ctas);
+  p.ids = ids; p.weights = weights; p.counts = counts; p.order = order;
+  p.hist = static_cast<int32_t*>(workspace);
+  if (launch_ex(route_choose_kernel, dim3(ctas), dim3(kRouteThreads), 0, s, true, 1, p) != cudaSuccess)
+    return MACAQ_ERR_CUDA;
+  if (counts == nullptr || ctas == 1) return MACAQ_OK;
+  return launch_ex(route_place_kernel, dim3(ctas), dim3(kRouteThreads), 0, s, true, 1, p) == cudaSuccess
+             ? MACAQ_OK
+             : MACAQ_ERR_CUDA;
+}
+
+// ---- mixture-of-experts layer for a few tokens ----
+// Shared memory of one kernel: as many token buffers as fit in half an SM's shared memory, so that
+// a CTA of each kernel fits on an SM together; failing that, what fits at all.
+static moe::Layout moe_layout(int T, int k, int E, int K, bool down) {
+  constexpr int kHalf = 113 * 1024;
+  for (const int limit : {kHalf, static_cast<int>(gemm::kSmemLimit)})
+    for (const int stages : {4, 3})
+      for (const int bufs : {4, 2, 1}) {
+        const moe::Layout l = moe::layout(T, k, E, K, down, stages, bufs);
+        if (l.bytes <= limit && moe::scratch_bytes(T, k, E) <= l.b) return l;
+      }
+  return moe::Layout{};
+}
+
+size_t macaq_moe_workspace_bytes(int64_t T, int64_t k, int64_t I) {
+  if (T < 1 || T > moe::kMaxTokens || k < 1 || k > moe::kMaxChoice || I < 256 || I > moe::kMaxK || I % 256 != 0) return 0;
+  return static_cast<size_t>(T) * k * I * 2;
+}
+
+int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const float* D_up, const uint8_t* Wq_up,
+                 const uint8_t* Ws_up, const float* D_down, const uint8_t* Wq_down, const uint8_t* Ws_down, int64_t T,
+                 int64_t E, int64_t k, int64_t H, int64_t I, int score, int renorm, float scale, int act_type,
+                 uint16_t* y, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  int st = check_rule(logits_type, E, k, moe::kMaxExperts, moe::kMaxChoice, score, scale);
+  if (st != MACAQ_OK) return st;
+  if (act_type != 2 && act_type != 5) return MACAQ_ERR_ACT_TYPE;
+  if (T < 0 || T > moe::kMaxTokens || H < 256 || H > moe::kMaxK || H % 256 != 0 || I < 256 || I > moe::kMaxK ||
+      I % 256 != 0)
+    return MACAQ_ERR_SHAPE;
+  if (T == 0) return MACAQ_OK;
+  if (!x || !logits || !D_up || !Wq_up || !Ws_up || !D_down || !Wq_down || !Ws_down || !y) return MACAQ_ERR_NULL;
+  const size_t xb = static_cast<size_t>(T) * H * 2, lb = static_cast<size_t>(T) * E * element_bytes(logits_type);
+  const size_t need = macaq_moe_workspace_bytes(T, k, I);
+  const struct { const void* p; size_t n; } in[] = {
+      {x, xb}, {logits, lb}, {D_up, static_cast<size_t>(E) * H * 4}, {Wq_up, macaq_weight_code_bytes(E, 2 * I, H)},
+      {Ws_up, macaq_weight_scale_bytes(E, 2 * I, H)}, {D_down, static_cast<size_t>(E) * I * 4},
+      {Wq_down, macaq_weight_code_bytes(E, H, I)}, {Ws_down, macaq_weight_scale_bytes(E, H, I)}};
+  for (const auto& i : in)
+    if (!aligned16(i.p)) return MACAQ_ERR_ALIGN;
+  if (!aligned16(y)) return MACAQ_ERR_ALIGN;
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return MACAQ_ERR_WORKSPACE;
+  for (const auto& i : in)
+    if (overlaps(y, xb, i.p, i.n) || overlaps(workspace, need, i.p, i.n)) return MACAQ_ERR_ALIAS;
+  if (overlaps(y, xb, workspace, need)) return MACAQ_ERR_ALIAS;
+  int dev, sms;
+  st = current_device(dev, sms);
+  if (st != MACAQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int t = static_cast<int>(T), kk = static_cast<int>(k), e = static_cast<int>(E);
+  MoeParams up{};
+  up.rule = route_rule(logits, logits_type, E, k, score, renorm, scale);
+  up.Wq = Wq_up; up.Ws = Ws_up; up.D = D_up; up.a = x; up.out = static_cast<uint16_t*>(workspace);
+  up.T = t; up.N = static_cast<int>(2 * I); up.K = static_cast<int>(H);
+  up.NT = up.N / kRowsTile; up.KT = up.K / kKTile;
+  up.gelu = act_type == 2 ? 1 : 0;
+  up.S = 1;
+  up.team = 4;
+  up.status = status;
+  up.l = moe_layout(t, kk, e, up.K, false);
+  MoeParams down = up;
+  down.Wq = Wq_down; down.Ws = Ws_down; down.D = D_down; down.a = static_cast<const uint16_t*>(workspace); down.out = y;
+  down.N = static_cast<int>(H); down.K = static_cast<int>(I);
+  down.NT = down.N / kRowsTile; down.KT = down.K / kKTile;
+  down.l = moe_layout(t, kk, e, down.K, true);
+  if (up.l.bytes == 0 || down.l.bytes == 0) return MACAQ_ERR_SHAPE;
+  // quantiser warps per group in the down kernel: one warp covers 512 channels of a row at a time;
+  // several teams need a buffer each
+  down.team = down.K <= 1024 ? 1 : down.K <= 2048 ? 2 : 4;
+  while (4 / down.team > down.l.bufs) down.team *= 2;
+  // at most T k groups (and an expert's further ones): more CTAs than that would have nothing to do
+  const int groups = moe::max_groups(t, kk, e);
+  const int items = groups * up.NT;
+  down.S = 8;
+  while (down.S > 1 && (down.S > groups || down.S * down.NT > sms)) down.S /= 2;
+  if (launch_ex(moe_kernel<false>, dim3(std::min(items, sms)), dim3(moe::kThreads), up.l.bytes, s, true, 1, up) !=
+      cudaSuccess)
+    return MACAQ_ERR_CUDA;
+  return launch_ex(moe_kernel<true>, dim3(down.S * down.NT), dim3(moe::kThreads), down.l.bytes, s, true, down.S,
+                   down) == cudaSuccess
+             ? MACAQ_OK
+             : MACAQ_ERR_CUDA;
 }
 
 }  // extern "C"
