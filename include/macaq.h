@@ -348,8 +348,10 @@ int macaq_prepare_gate_up(const float *W_dev, const float *D_dev, int64_t E, int
  *   D_down_dev fp32 [E, I]; Wq_down/Ws_down from macaq_prepare_weights(E, H, I);
  *   act_type 5 (SILU) or 2 (GELU_TANH), else MACAQ_ERR_ACT_TYPE;
  *   y_dev bf16 [T, H]; workspace: macaq_moe_workspace_bytes(T, k, I) bytes
- *   (the activations a); nothing in it has to start at zero, and calls that
- *   share it must not run concurrently.
+ *   (the activations a, quantised: codes [T k, I / 2] in canonical order as in
+ *   macaq_quantize_activations, then scales [T k, I / 32], row t k + j, rows of
+ *   weight zero not written; then tables); nothing in it has to start at zero, and calls
+ *   that share it must not run concurrently.
  *   The activation is evaluated with an FP32 exponential and division.
  * Shapes: 0 <= T <= 128; 1 <= E <= 512; 1 <= k <= min(E, 16); H and I multiples
  * of 256 in [256, 8192]. */

@@ -1,16 +1,20 @@
 """moe_mm, the mixture-of-experts layer for a few tokens, against its formula in 64 bits.
 
-The layer quantises twice, and a value on a border of the four-bit grid may fall on
-either side of it, so the two halves are checked one after the other; the activations
-between them are in the workspace.
-  a:  the up linear's codes are bit-exact (the oracle's), its products are summed in
-      FP32: K additions, each within 2^-23 of the running sum of magnitudes S, give
-      d = K 2^-23 S for gate and up.  act(g) u moves by at most (1.13 |u| + |act(g)|) d
-      (the slopes of SILU and GELU stay below 1.13), the exponential and the division
-      add (4 + |z|) 2^-22 of |act(g) u|, then one rounding to bf16 (2^-8).
-  y:  from the activations that the call left, K 2^-23 S per expert weighted by |w|,
-      eight products and sums of the experts (k + 2) 2^-23 sum |w y|, the weights'
-      own error (2^-17, tests of routing) and one rounding to bf16.
+The layer quantises twice, and a value on a border of a rounding may fall on either
+side of it, so the two halves are checked one after the other; the quantised
+activations between them are in the workspace.  The up linear's codes are bit-exact
+(the oracle's).  The products of 32 four-bit codes add up exactly, so a linear rounds
+K / 32 times, each within 2^-23 of the running sum of magnitudes S: d = K / 32 x 2^-23 S.
+  a:  act(g) u moves by at most (1.13 |u| + |act(g)|) d (the slopes of SILU and GELU
+      stay below 1.13), the exponential and the division add (4 + |z|) 2^-22 of it.
+      Where the whole interval rounds to one bf16 value for each of a block's 32
+      elements, the block's codes and scale must be the oracle's.  Elsewhere a value may
+      move by a step of bf16, its scaled value by that and one more rounding, the rotated
+      ones by the sum of these and a rounding; both encodings are within two units of
+      their scale of what they encode (saturation at 6 of up to 8).
+  y:  from the codes that the call left, d per expert weighted by |w|, k + 2 products
+      and sums of the experts, (k + 2) 2^-23 sum |w y|, the weights' own error (2^-17,
+      tests of routing) and one rounding to bf16 (2^-8).
 """
 import numpy as np
 import pytest
@@ -59,15 +63,37 @@ class Layer:
         return torch.from_numpy((scale * rng.standard_normal((T, self.E))).astype(np.float32)).cuda()
 
 
-def linear(bits, D, values):
-    """The exact products of quantised activations [n, K] with dequantised weights [N, K]; and the sums of magnitudes."""
-    a = oracle.dequantize(*oracle.quantize_act(np.ascontiguousarray(bits), D))
-    return (a @ values.T) / 32, (np.abs(a) @ np.abs(values).T) / 32
+def product(a, values):
+    """The exact products of dequantised activations [n, K] and weights [N, K], and what FP32 sums may be off."""
+    return (a @ values.T) / 32, a.shape[1] / 32 * 2.0 ** -23 * (np.abs(a) @ np.abs(values).T) / 32
 
 
 def activation(g, act):
     z = g if act == mq.ACT_SILU else 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
     return g / (1 + np.exp(-z)), np.abs(z)
+
+
+def bf16(v):
+    return synth.bf16_bits_to_f32(oracle.f64_to_bf16(v)).astype(np.float64)
+
+
+def check_activations(codes, scales, a, tol, D):
+    """The stored operand [n, K] against the activations a +- tol; returns its values."""
+    lo, mid, hi = bf16(a - tol), bf16(a), bf16(a + tol)
+    want_codes, want_scales = oracle.quantize_act(oracle.f64_to_bf16(a), D)
+    n, K = a.shape
+    free = (lo != hi).reshape(n, K // 32, 32)
+    same = ~free.any(-1)
+    assert (scales == want_scales)[same].all()
+    assert (codes.reshape(n, -1, 16) == want_codes.reshape(n, -1, 16)).all(-1)[same].all()
+    got, want = oracle.dequantize(codes, scales), oracle.dequantize(want_codes, want_scales)
+    r = np.abs(1 / D.astype(np.float64))
+    moved = ((hi - lo) * r + 2.0 ** -7 * np.abs(mid) * r).reshape(n, K // 32, 32)
+    moved = np.where(free, moved, 0).sum(-1)
+    top = np.exp2(np.maximum(scales, want_scales).astype(np.float64) - 127)
+    bound = moved + 2.0 ** -7 * 8 * top + 4 * top
+    assert (np.abs(got - want).reshape(n, -1, 32).max(-1) <= bound)[~same].all()
+    return got, same.mean()
 
 
 def check(layer, bits, x, logits, k, act=mq.ACT_SILU, **route):
@@ -79,29 +105,32 @@ def check(layer, bits, x, logits, k, act=mq.ACT_SILU, **route):
     assert status[0].item() == 0
     ids, w, _, _ = mq.moe_route(logits, k, sort=False, **route)
     ids, w = ids.cpu().numpy(), w.double().cpu().numpy()
-    inner = ws[: T * k * I * 2].view(torch.int16).cpu().numpy().view(np.uint16).reshape(T, k, I)
-    want, off, size = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
+    ws = ws.cpu().numpy()
+    codes = ws[: T * k * I // 2].reshape(T, k, I // 2)
+    scales = ws[T * k * I // 2 : T * k * I * 17 // 32].reshape(T, k, I // 32)
+    want, off, size, exact = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H)), []
     for e in range(layer.E):
         t, j = np.nonzero((ids == e) & (w != 0))
         if not len(t):
             continue
-        both, s = linear(bits[t], layer.d_up[e], layer.values(layer.w_up, layer.d_up, e))
-        d = H * 2.0 ** -23 * s
+        up = oracle.dequantize(*oracle.quantize_act(np.ascontiguousarray(bits[t]), layer.d_up[e]))
+        both, d = product(up, layer.values(layer.w_up, layer.d_up, e))
         g, u, dg, du = both[:, :I], both[:, I:], d[:, :I], d[:, I:]
         f, z = activation(g, act)
-        tol = 1.13 * (np.abs(u) + du) * dg + np.abs(f) * du + (4 + z) * 2.0 ** -22 * np.abs(f * u)
-        tol = tol + 2.0 ** -8 * (np.abs(f * u) + tol) + 2.0 ** -130
-        got = synth.bf16_bits_to_f32(inner[t, j]).astype(np.float64)
-        assert (np.abs(got - f * u) <= tol).all(), (e, np.max(np.abs(got - f * u) / tol))
-        part, s = linear(inner[t, j], layer.d_down[e], layer.values(layer.w_down, layer.d_down, e))
+        tol = 1.13 * (np.abs(u) + du) * dg + np.abs(f) * du + (4 + z) * 2.0 ** -22 * np.abs(f * u) + 2.0 ** -130
+        inner, share = check_activations(codes[t, j], scales[t, j], f * u, tol, layer.d_down[e])
+        exact.append(share)
+        part, d = product(inner, layer.values(layer.w_down, layer.d_down, e))
         we = w[t, j][:, None]
         want[t] += we * part
-        off[t] += np.abs(we) * I * 2.0 ** -23 * s
+        off[t] += np.abs(we) * d
         size[t] += np.abs(we * part)
     off += ((k + 2) * 2.0 ** -23 + 2.0 ** -17) * size
     off += 2.0 ** -8 * (np.abs(want) + off)
     got = y.double().cpu().numpy()
     assert (np.abs(got - want) <= off).all(), np.max(np.abs(got - want) / np.maximum(off, 1e-300))
+    # rows of weight zero are not written
+    assert (codes[w == 0] == 0xFF).all() and (scales[w == 0] == 0xFF).all()
     return y
 
 

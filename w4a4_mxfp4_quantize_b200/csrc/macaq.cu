@@ -1719,6 +1719,10 @@ int current_device(int& dev, int& sms) {
                    cudaSuccess;
     ok = ok && cudaFuncSetAttribute(moe_kernel<false>, a, gs) == cudaSuccess &&
          cudaFuncSetAttribute(moe_kernel<true>, a, gs) == cudaSuccess;
+    // a CTA of each on one SM needs all of it as shared memory, whichever comes first
+    const auto carve = cudaFuncAttributePreferredSharedMemoryCarveout;
+    ok = ok && cudaFuncSetAttribute(moe_kernel<false>, carve, cudaSharedmemCarveoutMaxShared) == cudaSuccess &&
+         cudaFuncSetAttribute(moe_kernel<true>, carve, cudaSharedmemCarveoutMaxShared) == cudaSuccess;
     if (!ok) return MACAQ_ERR_CUDA;
     s.attrs_set = true;
   }
@@ -2701,22 +2705,62 @@ int macaq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, i
 }
 
 // ---- mixture-of-experts layer for a few tokens ----
-// Shared memory of one kernel: as many token buffers as fit in half an SM's shared memory, so that
-// a CTA of each kernel fits on an SM together; failing that, what fits at all.
-static moe::Layout moe_layout(int T, int k, int E, int K, bool down) {
-  constexpr int kHalf = 113 * 1024;
-  for (const int limit : {kHalf, static_cast<int>(gemm::kSmemLimit)})
-    for (const int stages : {4, 3})
-      for (const int bufs : {4, 2, 1}) {
-        const moe::Layout l = moe::layout(T, k, E, K, down, stages, bufs);
-        if (l.bytes <= limit && moe::scratch_bytes(T, k, E) <= l.b) return l;
+// Shared memory of the two kernels.  A CTA of each on one SM lets the down kernel choose and start its
+// weight stream while the up kernel runs, so they share an SM's memory where they fit (`together`); the
+// up kernel takes what the down kernel leaves, weight stages first.
+static bool moe_layouts(int T, int k, int E, int H, int I, moe::Layout& up, moe::Layout& down, bool& together) {
+  constexpr int kSm = 228 * 1024, kReserved = 1024;  // per SM, and per resident CTA
+  constexpr int kLimit = static_cast<int>(gemm::kSmemLimit);
+  const int scratch = moe::scratch_bytes(T, k, E);
+  auto pick = [&](int K, bool is_down, int limit, int least, moe::Layout& l) {
+    for (int stages = moe::kMaxStages; stages >= least; --stages)
+      for (const int bufs : {is_down ? 4 : 2, is_down ? 2 : 1, 1}) {
+        l = moe::layout(T, k, E, K, is_down, stages, bufs);
+        if (l.bytes <= std::min(limit, kLimit) && scratch <= l.b) return true;
       }
-  return moe::Layout{};
+    return false;
+  };
+  down = moe::layout(T, k, E, I, true, 3, 4);
+  together = scratch <= down.b && pick(H, false, kSm - 2 * kReserved - down.bytes, 4, up);
+  return together || (pick(H, false, kLimit, 3, up) && pick(I, true, kLimit, 3, down));
+}
+// Bytes of the groups' tables in the workspace: a bound for every E.
+static size_t moe_table_bytes(int64_t T, int64_t k) {
+  const size_t tk = static_cast<size_t>(T) * k;
+  return 3 * 16 + 8 * tk + 8 * (tk + tk / moe::kRows) + 32;
+}
+
+// Clusters of S CTAs of the down kernel that the device holds at once, with `bytes` of shared memory
+// each; asked once per device, S and whole number of KiB.
+static int moe_clusters(int dev, int S, int bytes) {
+  static int16_t cache[kMaxDevices][8][228] = {};
+  const int kib = (bytes + 1023) / 1024;
+  int16_t& v = cache[dev][S - 1][kib - 1];
+  if (v == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(moe::kDownThreads);
+    cfg.dynamicSmemBytes = std::min<size_t>(static_cast<size_t>(kib) * 1024, gemm::kSmemLimit);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = S;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, moe_kernel<true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 1;
+    }
+    v = static_cast<int16_t>(std::max(1, std::min(n, 32767)));
+  }
+  return v;
 }
 
 size_t macaq_moe_workspace_bytes(int64_t T, int64_t k, int64_t I) {
   if (T < 1 || T > moe::kMaxTokens || k < 1 || k > moe::kMaxChoice || I < 256 || I > moe::kMaxK || I % 256 != 0) return 0;
-  return static_cast<size_t>(T) * k * I * 2;
+  return static_cast<size_t>(T) * k * (I / 2 + I / 32) + moe_table_bytes(T, k);  // codes, scales, tables
 }
 
 int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const float* D_up, const uint8_t* Wq_up,
@@ -2749,35 +2793,34 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   if (st != MACAQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int t = static_cast<int>(T), kk = static_cast<int>(k), e = static_cast<int>(E);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeParams up{};
   up.rule = route_rule(logits, logits_type, E, k, score, renorm, scale);
-  up.Wq = Wq_up; up.Ws = Ws_up; up.D = D_up; up.a = x; up.out = static_cast<uint16_t*>(workspace);
+  up.Wq = Wq_up; up.Ws = Ws_up; up.D = D_up; up.D_next = D_down; up.x = x;
+  up.codes = ws; up.scales = ws + static_cast<size_t>(T) * k * (I / 2);
   up.T = t; up.N = static_cast<int>(2 * I); up.K = static_cast<int>(H);
   up.NT = up.N / kRowsTile; up.KT = up.K / kKTile;
   up.gelu = act_type == 2 ? 1 : 0;
   up.S = 1;
-  up.team = 4;
   up.status = status;
-  up.l = moe_layout(t, kk, e, up.K, false);
   MoeParams down = up;
-  down.Wq = Wq_down; down.Ws = Ws_down; down.D = D_down; down.a = static_cast<const uint16_t*>(workspace); down.out = y;
+  down.Wq = Wq_down; down.Ws = Ws_down; down.y = y;
   down.N = static_cast<int>(H); down.K = static_cast<int>(I);
   down.NT = down.N / kRowsTile; down.KT = down.K / kKTile;
-  down.l = moe_layout(t, kk, e, down.K, true);
-  if (up.l.bytes == 0 || down.l.bytes == 0) return MACAQ_ERR_SHAPE;
-  // quantiser warps per group in the down kernel: one warp covers 512 channels of a row at a time;
-  // several teams need a buffer each
-  down.team = down.K <= 1024 ? 1 : down.K <= 2048 ? 2 : 4;
-  while (4 / down.team > down.l.bufs) down.team *= 2;
+  bool together = false;
+  if (!moe_layouts(t, kk, e, up.K, down.K, up.l, down.l, together)) return MACAQ_ERR_SHAPE;
+  if (!together) up.tables = down.tables = ws + static_cast<size_t>(T) * k * (I / 2 + I / 32);
   // at most T k groups (and an expert's further ones): more CTAs than that would have nothing to do
   const int groups = moe::max_groups(t, kk, e);
   const int items = groups * up.NT;
-  down.S = 8;
-  while (down.S > 1 && (down.S > groups || down.S * down.NT > sms)) down.S /= 2;
-  if (launch_ex(moe_kernel<false>, dim3(std::min(items, sms)), dim3(moe::kThreads), up.l.bytes, s, true, 1, up) !=
+  // the largest cluster of which all fit at once (of 8, 15 do: at 2048 channels clusters of 7 take 112 SMs,
+  // where 16 clusters of 8 would run one of them alone at the end and clusters of 4 take 64)
+  down.S = std::min(8, groups);
+  while (down.S > 1 && moe_clusters(dev, down.S, down.l.bytes) < down.NT) --down.S;
+  if (launch_ex(moe_kernel<false>, dim3(std::min(items, sms)), dim3(moe::kUpThreads), up.l.bytes, s, true, 1, up) !=
       cudaSuccess)
     return MACAQ_ERR_CUDA;
-  return launch_ex(moe_kernel<true>, dim3(down.S * down.NT), dim3(moe::kThreads), down.l.bytes, s, true, down.S,
+  return launch_ex(moe_kernel<true>, dim3(down.S * down.NT), dim3(moe::kDownThreads), down.l.bytes, s, true, down.S,
                    down) == cudaSuccess
              ? MACAQ_OK
              : MACAQ_ERR_CUDA;

@@ -1,6 +1,7 @@
 // A whole mixture-of-experts layer for a few tokens (T <= 128), in two kernels:
 //   up:   choose each token's experts from its logits; for every chosen expert e and
-//         its tokens  (g, u) = 2^-5 Q(H(x / D1_e)) . W1_e^T,  a = RNE_bf16(act(g) u)
+//         its tokens  (g, u) = 2^-5 Q(H(x / D1_e)) . W1_e^T,  a = RNE_bf16(act(g) u),
+//         stored as the MXFP4 operand Q(H(a / D2_e)) of the second linear
 //   down: y[t] = RNE_bf16( sum_e w[t, e] 2^-5 Q(H(a / D2_e)) . W2_e^T )
 // Reading the chosen experts' weights once is what the layer costs: 17/32 byte per
 // weight, against at most 16 tokens' worth of arithmetic per byte, so everything
@@ -11,66 +12,75 @@
 // groups out evenly, in order, so a CTA quantises its tokens for an expert once and
 // keeps them in shared memory for all of that expert's tiles it owns.  In the down
 // kernel a cluster of S CTAs owns 128 output channels; its CTAs share the groups,
-// each adds its own into an FP32 tile, and the S tiles are added in rank order
+// each adds its own into an FP32 tile, and the S tiles are added in a fixed order
 // through distributed shared memory: no atomics, no partial sums in memory.
 //
 // Both kernels choose the experts themselves (an integer selection, identical in
 // every CTA), so the down kernel needs nothing from the up kernel but the
 // activations a: launched as a programmatic dependent, it streams its first weight
-// tiles while the up kernel still runs.
+// tiles while the up kernel still runs.  The activations are quantised where they
+// are made: in the down kernel every one of its N / 128 tiles would do it again.
 //
-// Warps: 0 weight copies, 1 MMA, 2 scale copies, 4-7 epilogue, 8-11 activation
-// quantiser; all of them choose experts first.
+// Warps: 0 weight copies, 1 MMA, 2 scale copies, 4-7 epilogue; up: 8-15 quantise x;
+// down: 3 gathers the activations.  All of them choose experts first.
 #pragma once
 #include "route.cuh"
 
 namespace macaq {
 
 namespace moe {
-constexpr int kThreads = 384;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 16;         // tokens of a group: the MMA's N
+constexpr int kUpThreads = 512;
+constexpr int kDownThreads = 256;
+constexpr int kQuantThreads = 256;  // of the up kernel, from warp 8 on
+constexpr int kRows = 16;           // tokens of a group: the MMA's N
 constexpr int kMaxTokens = 128;
 constexpr int kMaxChoice = 16;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxK = 8192;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 4;
 constexpr int kBCodeBytes = kRows * 128;  // codes of one K tile of a group
 constexpr int kBSfBytes = 512;            // its scales: two blocks of 16 rows x 16 bytes
 constexpr int kStageBytes = kTileCodeBytes + kTileSfBytes;
-constexpr int kTmemCols = 128;            // two accumulators of 16 columns, then 16 scale columns a stage
+constexpr int kTmemCols = 256;            // two accumulators of 16 columns, then 16 scale columns a stage
 constexpr int kSfCol = 32;
 constexpr int kBarBytes = 512;
+// up: reciprocals of D for 2048 channels at a time, half blocks 20 floats apart (lanes that
+// read 16 bytes of the same place in eight neighbouring half blocks meet no bank twice)
+constexpr int kRcpChunk = 2048;
+constexpr int kRcpStride = 20;
+constexpr int kRcpBytes = kRcpChunk / 16 * kRcpStride * 4;
+// up: an item's activations, 16 tokens x 64 channels of bf16, rows 144 bytes apart
+constexpr int kActStride = 72;
+constexpr int kActBytes = kRows * kActStride * 2;
 static_assert(kSfCol + 16 * kMaxStages <= kTmemCols, "tensor memory");
 
 // Shared memory of one CTA, byte offsets from a 1024-byte boundary.
 struct Layout {
   int stages, bufs;
-  int sf, b, bsf, bar, ent, ent_tok, ent_w, grp, acc, bytes;
+  int sf, b, bsf, bar, ent, ent_tok, ent_w, grp, extra, bytes;
 };
 __host__ __device__ inline int max_groups(int T, int k, int E) {
   return (T * k < E ? T * k : E) + T * k / kRows;
 }
 __host__ __device__ inline int align16i(int v) { return (v + 15) & ~15; }
 // Bytes of the tables that only choosing needs; they lie where the weight stages come later.
-__host__ __device__ inline int scratch_bytes(int T, int k, int E) { return align16i(T * k * 6) + E * 20; }
+__host__ __device__ inline int scratch_bytes(int T, int k, int E) { return align16i(T * k * 6) + E * 20 + kUpThreads / 32 * 512; }
 __host__ inline Layout layout(int T, int k, int E, int K, bool down, int stages, int bufs) {
   const int KT = K / kKTile, tk = T * k, G = max_groups(T, k, E);
   Layout l;
   l.stages = stages;
   l.bufs = bufs;
   l.sf = stages * kTileCodeBytes;
-  l.b = l.sf + stages * kTileSfBytes;
-  l.b = (l.b + 1023) & ~1023;
+  l.b = (l.sf + stages * kTileSfBytes + 1023) & ~1023;
   l.bsf = l.b + bufs * KT * kBCodeBytes;
   l.bar = l.bsf + bufs * KT * kBSfBytes + 256;  // the last scale copy reads 256 bytes past its rows
   l.ent = l.bar + kBarBytes;
   l.ent_tok = l.ent + align16i(tk * 2);
   l.ent_w = l.ent_tok + align16i(tk * 2);
   l.grp = l.ent_w + align16i(tk * 4);
-  l.acc = l.grp + align16i(G * 8);
-  l.bytes = l.acc + (down ? T * kRowsTile * 4 : 0) + 1024;
+  l.extra = l.grp + align16i(G * 8);  // down: the FP32 tile; up: activations and reciprocals
+  l.bytes = l.extra + (down ? T * kRowsTile * 4 : 2 * kActBytes + 2 * kRcpBytes) + 1024;
   return l;
 }
 }  // namespace moe
@@ -79,13 +89,17 @@ struct MoeParams {
   RouteRule rule;
   const uint8_t* Wq;     // weight images of this kernel's linear
   const uint8_t* Ws;
-  const float* D;        // [E, K]
-  const uint16_t* a;     // up: x bf16 [T, K]; down: a bf16 [T k, K]
-  uint16_t* out;         // up: a bf16 [T k, N / 2]; down: y bf16 [T, N]
+  const float* D;        // up: [E, K]
+  const float* D_next;   // up: the second linear's [E, N / 2]
+  const uint16_t* x;     // up: bf16 [T, K]
+  uint8_t* codes;        // the activations' MXFP4 codes [T k, I / 2]: up writes them, down reads them
+  uint8_t* scales;       // and scales [T k, I / 32]
+  uint16_t* y;           // down: bf16 [T, N]
   int T, N, K, NT, KT;
   int gelu;              // up: act is GELU_TANH (else SILU)
+  uint8_t* tables;       // the groups' tables, copied from the up kernel's first CTA (nullptr: the down
+                         // kernel chooses for itself, while the up kernel runs)
   int S;                 // down: CTAs of a cluster
-  int team;              // quantiser warps that share a group (1, 2 or 4)
   int32_t* status;
   moe::Layout l;
 };
@@ -99,48 +113,108 @@ __device__ __forceinline__ float gated(float g, float u, int gelu) {
   return __fdividef(g, 1.0f + __expf(-z)) * u;
 }
 
+// bar.sync over `n` threads that also tells them whether all of them passed true.
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t n, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float block_scale(uint32_t c) { return __uint_as_float((254u - min(c, 253u)) << 23); }
+
 // Half a 32-element activation block (16 bf16 values, their reciprocals of D) per lane,
-// lanes 2 i and 2 i + 1 together: the arithmetic of act_block step by step, its last
-// butterfly stage (h = 16) and the block maximum exchanged between the two lanes.
-__device__ __forceinline__ void act_half_block(const uint4 (&xv)[2], const float2 (&r2)[8], bool upper, uint2& codes,
-                                               uint32_t& scale) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(xv);
-  float2 P[8];
+// lanes 2 i and 2 i + 1 together, R rows side by side: the arithmetic of act_block step
+// by step, its last butterfly stage (h = 16) and the block maximum exchanged between the
+// two lanes.
+template <int R>
+__device__ __forceinline__ void act_half_blocks(const uint4 (&xv)[R][2], const float2 (&r2)[8], bool upper,
+                                                uint2 (&codes)[R], uint32_t (&scale)[R]) {
+  float2 P[R][8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t xs = f2_to_bf16x2(f2_mul(bf16x2_to_f2(w[j]), r2[j]));
-    const float v0 = bf16lo(xs), v1 = bf16hi(xs);
-    P[j] = f2(__fadd_rn(v0, v1), __fsub_rn(v0, v1));
-  }
+  for (int n = 0; n < R; ++n) {
+    const uint32_t w[8] = {xv[n][0].x, xv[n][0].y, xv[n][0].z, xv[n][0].w,
+                           xv[n][1].x, xv[n][1].y, xv[n][1].z, xv[n][1].w};
 #pragma unroll
-  for (int hp = 1; hp < 8; hp <<= 1) {
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t xs = f2_to_bf16x2(f2_mul(bf16x2_to_f2(w[j]), r2[j]));
+      const float v0 = bf16lo(xs), v1 = bf16hi(xs);
+      P[n][j] = f2(__fadd_rn(v0, v1), __fsub_rn(v0, v1));
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i & hp) continue;
-      const float2 a = P[i], b = P[i + hp];
-      P[i] = f2_add(a, b);
-      P[i + hp] = f2_sub(a, b);
+    for (int hp = 1; hp < 8; hp <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i & hp) continue;
+        const float2 a = P[n][i], b = P[n][i + hp];
+        P[n][i] = f2_add(a, b);
+        P[n][i + hp] = f2_sub(a, b);
+      }
     }
   }
   const float sign = upper ? -1.0f : 1.0f;  // lower lane: mine + other, upper lane: other - mine
   const float2 s2 = f2(sign, sign);
-  uint32_t u[8];
-  uint32_t m = 0;
+  float2 o[R][8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 o = f2(__shfl_xor_sync(0xffffffffu, P[j].x, 1), __shfl_xor_sync(0xffffffffu, P[j].y, 1));
-    u[j] = f2_to_bf16x2(ffma2(P[j], s2, o));  // the product by +-1 is exact: one rounding
-    m = max_u16x2(m, u[j] & 0x7FFF7FFFu);
+  for (int n = 0; n < R; ++n)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      o[n][j] = f2(__shfl_xor_sync(0xffffffffu, P[n][j].x, 1), __shfl_xor_sync(0xffffffffu, P[n][j].y, 1));
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    uint32_t u[8], m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      u[j] = f2_to_bf16x2(ffma2(P[n][j], s2, o[n][j]));  // the product by +-1 is exact: one rounding
+      m = max_u16x2(m, u[j] & 0x7FFF7FFFu);
+    }
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t c = e8m0_from_amax_bits(max(m & 0xFFFFu, m >> 16) << 16);
+    const float2 q2 = f2(block_scale(c), block_scale(c));
+    codes[n].x = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[0]), q2), f2_mul(bf16x2_to_f2(u[1]), q2),
+                           f2_mul(bf16x2_to_f2(u[2]), q2), f2_mul(bf16x2_to_f2(u[3]), q2));
+    codes[n].y = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[4]), q2), f2_mul(bf16x2_to_f2(u[5]), q2),
+                           f2_mul(bf16x2_to_f2(u[6]), q2), f2_mul(bf16x2_to_f2(u[7]), q2));
+    scale[n] = c;
   }
-  m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  const uint32_t c = e8m0_from_amax_bits(max(m & 0xFFFFu, m >> 16) << 16);
-  const float s = __uint_as_float((254u - min(c, 253u)) << 23);
-  const float2 q2 = f2(s, s);
-  codes.x = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[0]), q2), f2_mul(bf16x2_to_f2(u[1]), q2),
-                      f2_mul(bf16x2_to_f2(u[2]), q2), f2_mul(bf16x2_to_f2(u[3]), q2));
-  codes.y = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[4]), q2), f2_mul(bf16x2_to_f2(u[5]), q2),
-                      f2_mul(bf16x2_to_f2(u[6]), q2), f2_mul(bf16x2_to_f2(u[7]), q2));
-  scale = c;
+}
+
+// One 32-element block per warp, element `lane` of R rows: the same steps with every
+// butterfly stage an exchange between lanes.  The even lanes receive the byte of codes of
+// elements lane and lane + 1.
+template <int R>
+__device__ __forceinline__ void act_lane_blocks(const float (&x)[R], float r, uint32_t (&byte)[R], uint32_t (&scale)[R]) {
+  const int lane = threadIdx.x & 31;
+  float v[R];
+#pragma unroll
+  for (int n = 0; n < R; ++n) v[n] = __bfloat162float(__float2bfloat16_rn(__fmul_rn(x[n], r)));
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+    const float sign = (lane & h) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int n = 0; n < R; ++n) v[n] = __fmaf_rn(v[n], sign, __shfl_xor_sync(0xffffffffu, v[n], h));
+  }
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    const float u = __bfloat162float(__float2bfloat16_rn(v[n]));
+    const uint32_t c = e8m0_from_amax_bits(__reduce_max_sync(0xffffffffu, __float_as_uint(u) & 0x7FFFFFFFu));
+    const float q = __fmul_rn(u, block_scale(c));
+    byte[n] = e2m1x2(q, __shfl_xor_sync(0xffffffffu, q, 1));
+    scale[n] = c;
+  }
+}
+
+// A load that is issued where it stands, before the barrier that lets the weights follow.
+__device__ __forceinline__ float ld_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
 }
 
 // The groups of the call, from the logits (every CTA computes the same): ent[] lists the
@@ -148,63 +222,70 @@ __device__ __forceinline__ void act_half_block(const uint4 (&xv)[2], const float
 // 16 of them of one expert, grp = {first entry, expert | rows << 16}.  A pair of weight
 // zero is left out: it adds nothing and its expert need not be read.  Returns the number
 // of groups.  `scratch` overlaps the weight stages.
-__device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uint8_t* scratch, int* n_groups) {
+template <int kThreads>
+__device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uint8_t* scratch, int* warp_total) {
+  constexpr int kWarps = kThreads / 32;
   const int k = p.rule.k, E = p.rule.E, T = p.T, tk = T * k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* sel_w = reinterpret_cast<float*>(scratch);
   uint16_t* sel_e = reinterpret_cast<uint16_t*>(sel_w + tk);
   uint32_t* mask = reinterpret_cast<uint32_t*>(scratch + moe::align16i(tk * 6));  // [E][4]: tokens that chose e
   int* off = reinterpret_cast<int*>(mask + E * 4);                                // [E]: first entry
+  int* ids = off + E;                                                             // [kWarps][128]
   uint16_t* ent = reinterpret_cast<uint16_t*>(smem + p.l.ent);
   uint16_t* ent_tok = reinterpret_cast<uint16_t*>(smem + p.l.ent_tok);
   float* ent_w = reinterpret_cast<float*>(smem + p.l.ent_w);
   int2* grp = reinterpret_cast<int2*>(smem + p.l.grp);
-  for (int i = threadIdx.x; i < E * 4; i += moe::kThreads) mask[i] = 0u;
+  for (int i = threadIdx.x; i < E * 4; i += kThreads) mask[i] = 0u;
   __syncthreads();
-  for_keys_per_lane(E, [&](auto keys) {
-    if constexpr (decltype(keys)::value <= moe::kMaxExperts / 32) {
-      for (int t = warp; t < T; t += moe::kWarps) {
-        int e;
-        float w;
-        choose_experts<decltype(keys)::value>(p.rule, t, e, w);
-        if (lane < k) {
-          const bool used = w != 0.f;
-          sel_w[t * k + lane] = w;
-          sel_e[t * k + lane] = used ? static_cast<uint16_t>(e) : 0xFFFFu;
-          if (used) atomicOr(&mask[e * 4 + (t >> 5)], 1u << (t & 31));
-        }
-      }
-    }
+  for_spread<moe::kMaxExperts>(E, T <= kWarps, [&](auto spread) {
+    using S = decltype(spread);
+    // tokens warp, warp + kWarps, ...: few tokens are spread over the warps before they share one
+    for (int t = warp; t < T; t += kWarps * S::kTokens)
+      choose_experts<S>(p.rule, t, T, kWarps, ids + warp * 128, [&](int64_t tok, int j, int e, float w) {
+        const int at = static_cast<int>(tok) * k + j;
+        const bool used = w != 0.f;
+        sel_w[at] = w;
+        sel_e[at] = used ? static_cast<uint16_t>(e) : 0xFFFFu;
+        if (used) atomicOr(&mask[e * 4 + (static_cast<int>(tok) >> 5)], 1u << (tok & 31));
+      });
   });
   __syncthreads();
-  if (warp == 0) {  // entries and groups before each expert
-    int ent_base = 0, grp_base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      int c = 0;
-      if (e < E) {
-        const uint4 m = *reinterpret_cast<const uint4*>(mask + e * 4);
-        c = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
-      }
-      const int g = (c + moe::kRows - 1) / moe::kRows;
-      int both = c | (g << 16);  // at most 2048 entries and 128 + E groups: both sums stay below 2^15
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, both, o);
-        if (lane >= o) both += u;
-      }
-      const int c0 = ent_base + (both & 0xFFFF) - c, g0 = grp_base + (both >> 16) - g;
-      if (e < E) off[e] = c0;
-      for (int i = 0; i < g; ++i)
-        grp[g0 + i] = make_int2(c0 + i * moe::kRows, e | (min(moe::kRows, c - i * moe::kRows) << 16));
-      const int total = __shfl_sync(0xffffffffu, both, 31);
-      ent_base += total & 0xFFFF;
-      grp_base += total >> 16;
+  // entries and groups before each expert, one expert per thread
+  int ent_base = 0, grp_base = 0;
+  for (int e0 = 0; e0 < E; e0 += kThreads) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    int c = 0;
+    if (e < E) {
+      const uint4 m = *reinterpret_cast<const uint4*>(mask + e * 4);
+      c = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
     }
-    if (lane == 0) *n_groups = grp_base;
+    const int g = (c + moe::kRows - 1) / moe::kRows;
+    int both = c | (g << 16);  // at most 2048 entries and 640 groups: the sums stay apart
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) both += u;
+    }
+    if (lane == 31) warp_total[warp] = both;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int n = warp_total[w];
+      before += w < warp ? n : 0;
+      total += n;
+    }
+    both += before;
+    const int c0 = ent_base + (both & 0xFFFF) - c, g0 = grp_base + (both >> 16) - g;
+    if (e < E) off[e] = c0;
+    for (int i = 0; i < g; ++i)
+      grp[g0 + i] = make_int2(c0 + i * moe::kRows, e | (min(moe::kRows, c - i * moe::kRows) << 16));
+    ent_base += total & 0xFFFF;
+    grp_base += total >> 16;
+    __syncthreads();
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tk; i += moe::kThreads) {
+  for (int i = threadIdx.x; i < tk; i += kThreads) {
     const int e = sel_e[i];
     if (e != 0xFFFF) {
       const int t = i / k;
@@ -217,12 +298,14 @@ __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uin
   }
   fence_proxy_async_smem();  // the stages' copies will overwrite the scratch
   __syncthreads();
-  return *n_groups;
+  return grp_base;
 }
 
+// 80 registers: a CTA of each kernel on one SM is (512 + 256) x 80 of its 65536.
 template <bool kDown>
-__global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p) {
+__global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) {
   using namespace moe;
+  constexpr int kThreads = kDown ? kDownThreads : kUpThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.l.bar);
@@ -234,13 +317,12 @@ __global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_cons
   uint64_t* acce = accf + 2;              // [2]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acce + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  volatile int* epi_ok = abort_flag + 1;  // [4], one per epilogue warp
-  int* n_groups = reinterpret_cast<int*>(const_cast<int*>(epi_ok) + 4);
+  int* warp_total = const_cast<int*>(abort_flag) + 1;  // [kWarps], while the groups are formed
   const uint16_t* ent = reinterpret_cast<const uint16_t*>(smem + p.l.ent);
   const uint16_t* ent_tok = reinterpret_cast<const uint16_t*>(smem + p.l.ent_tok);
   const float* ent_w = reinterpret_cast<const float*>(smem + p.l.ent_w);
   const int2* grp = reinterpret_cast<const int2*>(smem + p.l.grp);
-  float* acc = reinterpret_cast<float*>(smem + p.l.acc);  // down: [T][128]
+  float* acc = reinterpret_cast<float*>(smem + p.l.extra);  // down: [T][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.l.stages, bufs = p.l.bufs;
 
@@ -255,7 +337,7 @@ __global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_cons
       mbar_init(&sfull[s], 1);
     }
     for (int b = 0; b < kMaxBufs; ++b) {
-      mbar_init(&bfull[b], p.team);
+      mbar_init(&bfull[b], kDown ? 1 : kQuantThreads / 32);
       mbar_init(&bempty[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -266,11 +348,30 @@ __global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_cons
     fence_mbar_init();
   }
   if constexpr (!kDown) {
-    pdl_wait();     // x and the logits may come from the kernel before
-    pdl_trigger();  // the down kernel may start: what it reads before its own wait is complete
+    pdl_wait();  // x and the logits may come from the kernel before
+    // The down kernel may start: what it reads before its own wait is complete.  Warp 1 says so, after
+    // its tensor memory is allocated: a CTA of the down kernel may take the rest of it and wait for us.
+    if (warp == 1) pdl_trigger();
   }
   tc_fence_before();
-  const int G = moe_groups(p, smem, smem, n_groups);
+  // ent, ent_tok, ent_w and grp are one run of shared memory from l.ent to l.extra, the same in both
+  // kernels; the count follows it in the copy
+  const int table_words = (p.l.extra - p.l.ent) / 16;
+  int G;
+  if (kDown && p.tables != nullptr) {
+    pdl_wait();
+    const uint4* src = reinterpret_cast<const uint4*>(p.tables);
+    for (int i = threadIdx.x; i < table_words; i += kThreads) reinterpret_cast<uint4*>(smem + p.l.ent)[i] = src[i];
+    G = *reinterpret_cast<const int*>(src + table_words);
+    __syncthreads();
+  } else {
+    G = moe_groups<kThreads>(p, smem, smem, warp_total);
+    if (!kDown && p.tables != nullptr && blockIdx.x == 0) {
+      uint4* dst = reinterpret_cast<uint4*>(p.tables);
+      for (int i = threadIdx.x; i < table_words; i += kThreads) dst[i] = reinterpret_cast<const uint4*>(smem + p.l.ent)[i];
+      if (threadIdx.x == 0) *reinterpret_cast<int*>(dst + table_words) = G;
+    }
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int KT = p.KT;
@@ -278,37 +379,62 @@ __global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_cons
   const int rank = kDown ? static_cast<int>(cluster_ctarank()) : 0;
   const int total = kDown ? G : G * p.NT;
   const int share = kDown ? rank : static_cast<int>(blockIdx.x), shares = kDown ? p.S : static_cast<int>(gridDim.x);
-  const int i0 = static_cast<int>(static_cast<int64_t>(total) * share / shares);
-  const int i1 = static_cast<int>(static_cast<int64_t>(total) * (share + 1) / shares);
-  const int tile0 = kDown ? static_cast<int>(blockIdx.x) / p.S : 0;
-  auto group_of = [&](int i) { return kDown ? i : i / p.NT; };
-  auto tile_of = [&](int i) { return kDown ? tile0 : i % p.NT; };
-  const int g0 = group_of(i0), g1 = i1 > i0 ? group_of(i1 - 1) + 1 : g0;  // this CTA's groups
+  // (at most 640 groups of 128 tiles times 148 shares: below 2^24)
+  const int i0 = static_cast<int>(static_cast<uint32_t>(total * share) / static_cast<uint32_t>(shares));
+  const int i1 = static_cast<int>(static_cast<uint32_t>(total * (share + 1)) / static_cast<uint32_t>(shares));
+  const int n_items = i1 - i0;
+  const int g0 = kDown ? i0 : i0 / p.NT, g1 = n_items <= 0 ? g0 : kDown ? i1 : (i1 - 1) / p.NT + 1;  // this CTA's groups
+  const int tile0 = kDown ? static_cast<int>(blockIdx.x) / p.S : i0 - g0 * p.NT;
+  // a role's walk over the items, no division in it: group (its buffer, the parity of the buffer's
+  // turn), tile, and whether this is the group's last item here
+  struct Walk {
+    int i = 0, g, tile, buf = 0;
+    uint32_t turn = 0;
+    bool fresh = true;  // first item of its group
+  };
+  auto walk = [&] {
+    Walk w;
+    w.g = g0;
+    w.tile = tile0;
+    return w;
+  };
+  auto last_of_group = [&](const Walk& w) { return kDown || w.tile + 1 == p.NT || w.i + 1 == n_items; };
+  auto next_item = [&](Walk& w) {
+    ++w.i;
+    w.fresh = kDown || w.tile + 1 == p.NT;
+    if (!kDown) w.tile = w.fresh ? 0 : w.tile + 1;
+    if (w.fresh) {
+      ++w.g;
+      if (++w.buf == bufs) {
+        w.buf = 0;
+        w.turn ^= 1;
+      }
+    }
+  };
 
   if (warp == 0) {
     // ---- producer: lane 0 copies a stage's weight codes, lane 1 its scales ----
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int i = i0; i < i1 && ok; ++i) {
-      const int e = grp[group_of(i)].y & 0xFFFF;
-      const size_t img = weight_image(e, tile_of(i), 0, p.NT / 2, KT);
+    // the first group's channel factors go ahead of the weights: behind them they would wait for as
+    // many bytes as the stages hold
+    if constexpr (!kDown) named_bar_sync(3, kQuantThreads + 32);
+    const uint64_t policy = l2_evict_first();  // read once: the rest of L2 keeps its lines
+    for (Walk w = walk(); w.i < n_items && ok; next_item(w)) {
+      const int e = grp[w.g].y & 0xFFFF;
+      const size_t img = weight_image(e, w.tile, 0, p.NT / 2, KT);
       const uint8_t* src = (lane & 1) ? p.Ws + img * kTileSfBytes : p.Wq + img * kTileCodeBytes;
       const uint32_t bytes = (lane & 1) ? kTileSfBytes : kTileCodeBytes;
       uint8_t* dst0 = (lane & 1) ? smem + p.l.sf : smem;
       for (int kt = 0; kt < KT; ++kt) {
-        int got = 1;
-        if (lane == 0) {
-          got = mbar_wait(&empty[stage], phase ^ 1, abort_flag, kWaitTimeoutNs) ? 1 : 0;
-          if (got) mbar_arrive_expect_tx(&full[stage], kStageBytes);
-        }
-        __syncwarp();  // the stage is free for both lanes
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, kWaitTimeoutNs)) {
           ok = false;
           break;
         }
-        bulk_g2s_if(lane < 2, dst0 + stage * bytes, src, bytes, &full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], kStageBytes);
+        __syncwarp();
+        bulk_g2s_hint_if(lane < 2, dst0 + stage * bytes, src, bytes, &full[stage], policy);
         src += 2 * bytes;  // the next K tile's image pair
         if (++stage == stages) {
           stage = 0;
@@ -317,70 +443,73 @@ __global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_cons
       }
     }
   } else if (warp == 1) {
-    // ---- MMA issuer ----
-    if (lane == 0) {
+    // ---- MMA issuer: the whole warp takes every step and one elected lane issues, so addresses and
+    // descriptors stay in uniform registers (a stage's four MMAs issue in 260 cycles, from a lone lane
+    // in 300, and its scale copies in 350, from a lone lane in 440) ----
+    {
       const uint32_t idesc_lo = idesc_mxf4(128, kRows, 0, 0), idesc_hi = idesc_mxf4(128, kRows, 2, 2);
       const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)), b0 = sdesc_kmajor_sw128(smem_u32(smem + p.l.b));
-      int stage = 0, g = -1, buf = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int i = i0; i < i1 && ok; ++i) {
-        const int ab = (i - i0) & 1;
-        if (group_of(i) != g) {
-          g = group_of(i);
-          buf = (g - g0) % bufs;
-          if (!mbar_wait(&bfull[buf], ((g - g0) / bufs) & 1, abort_flag, kWaitTimeoutNs)) break;
-        }
-        if (!mbar_wait(&acce[ab], (((i - i0) >> 1) & 1) ^ 1, abort_flag, kWaitTimeoutNs)) break;
+      for (Walk w = walk(); w.i < n_items && ok; next_item(w)) {
+        const int ab = w.i & 1;
+        if (w.fresh && !mbar_wait_warp(&bfull[w.buf], w.turn, abort_flag, kWaitTimeoutNs)) break;
+        if (!mbar_wait_warp(&acce[ab], ((w.i >> 1) & 1) ^ 1, abort_flag, kWaitTimeoutNs)) break;
         tc_fence_after();
         for (int kt = 0; kt < KT; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, kWaitTimeoutNs) ||
-              !mbar_wait(&sfull[stage], phase, abort_flag, kWaitTimeoutNs)) {
+          if (!mbar_wait_warp(&full[stage], phase, abort_flag, kWaitTimeoutNs) ||
+              !mbar_wait_warp(&sfull[stage], phase, abort_flag, kWaitTimeoutNs)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sf = tmem + kSfCol + 16 * stage;
-          mma_stage(a0 + (static_cast<uint32_t>(stage * kTileCodeBytes) >> 4),
-                    b0 + (static_cast<uint32_t>((buf * KT + kt) * kBCodeBytes) >> 4), sf, sf + 8, tmem + ab * kRows,
-                    idesc_lo, idesc_hi, kt == 0);
-          tc_commit(&empty[stage]);
+          if (elect_one()) {
+            mma_stage(a0 + (static_cast<uint32_t>(stage * kTileCodeBytes) >> 4),
+                      b0 + (static_cast<uint32_t>((w.buf * KT + kt) * kBCodeBytes) >> 4), sf, sf + 8, tmem + ab * kRows,
+                      idesc_lo, idesc_hi, kt == 0);
+            tc_commit(&empty[stage]);
+          }
+          __syncwarp();
           if (++stage == stages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        tc_commit(&accf[ab]);
-        if (i + 1 == i1 || group_of(i + 1) != g) tc_commit(&bempty[buf]);
+        if (elect_one()) {
+          tc_commit(&accf[ab]);
+          if (last_of_group(w)) tc_commit(&bempty[w.buf]);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == 2) {
     // ---- scale copies of a stage into its TMEM slot: weights 8 columns, tokens 8 columns ----
-    if (lane == 0) {
+    {
       const uint64_t sfa0 = sdesc_sf_block(smem_u32(smem + p.l.sf)), sfb0 = sdesc_sf_block(smem_u32(smem + p.l.bsf));
-      int stage = 0, g = -1, buf = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int i = i0; i < i1 && ok; ++i) {
-        if (group_of(i) != g) {
-          g = group_of(i);
-          buf = (g - g0) % bufs;
-          if (!mbar_wait(&bfull[buf], ((g - g0) / bufs) & 1, abort_flag, kWaitTimeoutNs)) break;
-        }
+      for (Walk w = walk(); w.i < n_items && ok; next_item(w)) {
+        if (w.fresh && !mbar_wait_warp(&bfull[w.buf], w.turn, abort_flag, kWaitTimeoutNs)) break;
         for (int kt = 0; kt < KT; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, kWaitTimeoutNs)) {
+          if (!mbar_wait_warp(&full[stage], phase, abort_flag, kWaitTimeoutNs)) {
             ok = false;
             break;
           }
           const uint32_t sf = tmem + kSfCol + 16 * stage;
           const uint64_t sa = sfa0 + (static_cast<uint32_t>(stage * kTileSfBytes) >> 4);
-          const uint64_t sb = sfb0 + (static_cast<uint32_t>((buf * KT + kt) * kBSfBytes) >> 4);
-          tc_cp_32x128b_warpx4(sf, sa);
-          tc_cp_32x128b_warpx4(sf + 4, sa + (512 >> 4));
-          tc_cp_32x128b_warpx4(sf + 8, sb);
-          tc_cp_32x128b_warpx4(sf + 12, sb + (256 >> 4));
-          tc_commit(&sfull[stage]);
+          const uint64_t sb = sfb0 + (static_cast<uint32_t>((w.buf * KT + kt) * kBSfBytes) >> 4);
+          if (elect_one()) {
+            tc_cp_32x128b_warpx4(sf, sa);
+            tc_cp_32x128b_warpx4(sf + 4, sa + (512 >> 4));
+            tc_cp_32x128b_warpx4(sf + 8, sb);
+            tc_cp_32x128b_warpx4(sf + 12, sb + (256 >> 4));
+            tc_commit(&sfull[stage]);
+          }
+          __syncwarp();
           if (++stage == stages) {
             stage = 0;
             phase ^= 1;
@@ -388,137 +517,262 @@ __global__ void __launch_bounds__(moe::kThreads, 2) moe_kernel(const __grid_cons
         }
       }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp == 3) {
+    if constexpr (kDown) {
+      // ---- the groups' activations into the tensor core's layout: codes in 16-byte pieces, scales in
+      // words of four blocks, `lag` groups in flight behind the one being issued ----
+      pdl_wait();  // they come from the up kernel
+      pdl_trigger();
+      const int n = g1 - g0, lag = bufs > 2 ? 2 : 0;
+      const int code_row = p.K / 2, sf_row = p.K / 32;
+      int buf = 0, done = 0;  // buffers of the group being issued and of the next to have landed
+      uint32_t turn = 1;
+      for (int i = 0; i < n + lag; ++i) {
+        if (i < n) {
+          if (!mbar_wait_warp(&bempty[buf], turn, abort_flag, kWaitTimeoutNs)) break;
+          const int2 gr = grp[g0 + i];
+          const int first = gr.x, rows = gr.y >> 16;
+          uint8_t* bq = smem + p.l.b + buf * KT * kBCodeBytes;
+          uint8_t* bs = smem + p.l.bsf + buf * KT * kBSfBytes;
+          // lane: piece c of row j, four rows at a time (lanes past the last row repeat it)
+          const int c = lane & 7;
+          for (int j0 = 0; j0 < rows; j0 += 4) {
+            const int j = min(j0 + (lane >> 3), rows - 1);
+            const int e = ent[first + j];
+            const uint8_t* src = p.codes + static_cast<int64_t>(e) * code_row + c * 16;
+            uint8_t* dst = bq + code_chunk_offset(j, c);
+#pragma unroll 4
+            for (int kt = 0; kt < KT; ++kt) cp_async16(dst + kt * kBCodeBytes, src + kt * 128);
+            const uint8_t* sf = p.scales + static_cast<int64_t>(e) * sf_row;
+            for (int w0 = 0; w0 < 2 * KT; w0 += 8) {
+              const int w = min(w0 + c, 2 * KT - 1);
+              cp_async4(bs + (w >> 1) * kBSfBytes + (w & 1) * 256 + j * 16, sf + w * 4);
+            }
+          }
+          if (++buf == bufs) {
+            buf = 0;
+            turn ^= 1;
+          }
+        }
+        cp_async_commit();
+        if (i >= lag) {
+          if (lag == 2) cp_async_wait<2>();
+          else cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bfull[done]);
+          if (++done == bufs) done = 0;
+        }
+      }
+      cp_async_wait<0>();  // no copy may still be writing this CTA's shared memory at exit
+    }
+  } else if (warp < 8) {
     // ---- epilogue: 16 accumulator columns (tokens) of this thread's weight row ----
     const int q = warp & 3, row = q * 32 + lane;
     if constexpr (kDown) {
       for (int t = 0; t < p.T; ++t) acc[t * kRowsTile + row] = 0.f;
     }
-    for (int i = i0; i < i1; ++i) {
-      const int ab = (i - i0) & 1;
-      if (lane == 0) epi_ok[q] = mbar_wait(&accf[ab], ((i - i0) >> 1) & 1, abort_flag, kWaitTimeoutNs) ? 1 : 0;
+    for (Walk w = walk(); w.i < n_items; next_item(w)) {
+      const int ab = w.i & 1;
+      const int2 gr = grp[w.g];
+      const int first = gr.x, e = gr.y & 0xFFFF, rows = gr.y >> 16;
+      // up: of the item's 64 channels warps 0 and 1 quantise the first block of 32, warps 2 and 3 the second
+      const int channel = w.tile * (kRowsTile / 2) + (q >> 1) * 32 + lane;
+      float rcp = 1.f;
+      if constexpr (!kDown) rcp = __frcp_rn(__ldg(p.D_next + static_cast<int64_t>(e) * (p.N / 2) + channel));
       __syncwarp();
-      if (!epi_ok[q]) break;
-      tc_fence_after();
+      const bool ok = mbar_wait_warp(&accf[ab], (w.i >> 1) & 1, abort_flag, kWaitTimeoutNs);
       uint32_t r[kRows];
-      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * kRows, r);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acce[ab]);
-      const int2 gr = grp[group_of(i)];
-      const int first = gr.x, rows = gr.y >> 16;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * kRows, r);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acce[ab]);
+      }
       if constexpr (kDown) {
+        if (!ok) break;
+        // the tokens of a group differ, so their sums are read together, then written
+        float* o[kRows];
+        float v[kRows];
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-          if (j < rows) {
-            float* o = acc + ent_tok[first + j] * kRowsTile + row;
-            *o = fmaf(ent_w[first + j] * 0.03125f, __uint_as_float(r[j]), *o);
-          }
+          const int jj = first + min(j, rows - 1);
+          o[j] = acc + ent_tok[jj] * kRowsTile + row;
+          v[j] = fmaf(ent_w[jj] * 0.03125f, __uint_as_float(r[j]), *o[j]);
         }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (j < rows) *o[j] = v[j];
       } else {
         // weight rows 2 c and 2 c + 1 are the gate and the up row of channel c: of two tokens
         // the even lane finishes the first, the odd lane the second
-        const bool odd = lane & 1;
-        const int64_t half = p.N / 2;
-        uint16_t* o = p.out + (tile_of(i) * kRowsTile + row) / 2;
+        uint16_t* act = reinterpret_cast<uint16_t*>(smem + p.l.extra + ab * kActBytes);
+        if (ok) {
+          const bool odd = lane & 1;
 #pragma unroll
-        for (int j = 0; j < kRows; j += 2) {
-          if (j < rows) {
-            const float a = __uint_as_float(r[j]) * 0.03125f, b = __uint_as_float(r[j + 1]) * 0.03125f;
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-            const float h = gated(odd ? other : a, odd ? b : other, p.gelu);
-            const int jj = j + (odd ? 1 : 0);
-            if (jj < rows) o[ent[first + jj] * half] = bf16_bits(h);
+          for (int j = 0; j < kRows; j += 2) {
+            if (j < rows) {
+              const float a = __uint_as_float(r[j]) * 0.03125f, b = __uint_as_float(r[j + 1]) * 0.03125f;
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+              act[(j + (odd ? 1 : 0)) * kActStride + (row >> 1)] =
+                  bf16_bits(gated(odd ? other : a, odd ? b : other, p.gelu));
+            }
           }
+        }
+        // (the two copies of `act` alternate: this barrier also separates an item's reads from
+        // the writes of the item after the next)
+        if (!named_bar_all(1, 128, ok)) break;
+        const uint16_t* mine = act + (q >> 1) * 32 + lane;
+        for (int j = q & 1; j < rows; j += 4) {  // tokens j and j + 2
+          const int j2 = min(j + 2, rows - 1);
+          const float h[2] = {bf16lo(mine[j * kActStride]), bf16lo(mine[j2 * kActStride])};
+          uint32_t byte[2], scale[2];
+          act_lane_blocks<2>(h, rcp, byte, scale);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (n == 0 || j + 2 < rows) {
+              const int64_t at = ent[first + (n == 0 ? j : j2)];
+              if (!(lane & 1)) p.codes[at * (p.N / 4) + channel / 2] = static_cast<uint8_t>(byte[n]);
+              if (lane == 0) p.scales[at * (p.N / 64) + channel / 32] = static_cast<uint8_t>(scale[n]);
+            }
+          }
+          __syncwarp();
         }
       }
     }
-  } else if (warp >= 8) {
-    // ---- activation quantiser: team m of `team` warps takes this CTA's groups m, m + teams, ... ----
-    if constexpr (kDown) {
-      pdl_wait();  // the activations come from the up kernel
-      pdl_trigger();
-    }
-    const int team = (warp - 8) / p.team, teams = 4 / p.team;
-    const int tt = (warp - 8) % p.team * 32 + lane, TT = p.team * 32;
-    const int HB = p.K / 16;  // half blocks of a row, two lanes to a block
-    const int split = HB < TT ? TT / HB : 1;  // threads left over take other rows
-    const int rs = HB < TT ? tt / HB : 0, hb0 = HB < TT ? tt % HB : tt;
-    const bool upper = lane & 1;
-    for (int g = g0 + team; g < g1; g += teams) {
-      const int buf = (g - g0) % bufs;
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait(&bempty[buf], (((g - g0) / bufs) & 1) ^ 1, abort_flag, kWaitTimeoutNs) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      const int2 gr = grp[g];
-      const int first = gr.x, e = gr.y & 0xFFFF, rows = gr.y >> 16;
-      uint8_t* bq = smem + p.l.b + buf * KT * kBCodeBytes;
-      uint8_t* bs = smem + p.l.bsf + buf * KT * kBSfBytes;
-      for (int hb = hb0; hb - hb0 < HB; hb += TT) {  // the same number of turns for every lane
-        const bool in = hb < HB && rs < split;
-        float2 r2[8] = {};
-        if (in) {
-          const float4* d = reinterpret_cast<const float4*>(p.D + static_cast<int64_t>(e) * p.K + hb * 16);
+  } else {
+    if constexpr (!kDown) {
+      // ---- x quantiser: all of its warps on one group after the other ----
+      const int tt = static_cast<int>(threadIdx.x) - 8 * 32;
+      const bool upper = lane & 1;
+      float* rcp0 = reinterpret_cast<float*>(smem + p.l.extra + 2 * kActBytes);
+      int turn = 0;
+      bool ok = true;
+      // the channel factors of a group's first chunk are loaded a group ahead
+      float d0[kRcpChunk / kQuantThreads];
+      auto load_d = [&](int g, int k0) {
+        const float* d = p.D + static_cast<int64_t>(grp[g].y & 0xFFFF) * p.K + k0;
+#pragma unroll
+        for (int i = 0; i < kRcpChunk / kQuantThreads; ++i) {
+          const int c = tt + i * kQuantThreads;
+          d0[i] = 1.0f;
+          if (k0 + c < p.K) d0[i] = ld_now(d + c);
+        }
+      };
+      if (g0 < g1) load_d(g0, 0);
+      asm volatile("bar.arrive 3, %0;" ::"n"(kQuantThreads + 32) : "memory");
+      int buf = 0;
+      uint32_t buf_turn = 1;
+      for (int g = g0; g < g1 && ok; ++g) {
+        const int2 gr = grp[g];
+        const int first = gr.x, rows = gr.y >> 16;
+        uint8_t* bq = smem + p.l.b + buf * KT * kBCodeBytes;
+        uint8_t* bs = smem + p.l.bsf + buf * KT * kBSfBytes;
+        ok = mbar_wait_warp(&bempty[buf], buf_turn, abort_flag, kWaitTimeoutNs);
+        for (int k0 = 0; k0 < p.K; k0 += kRcpChunk) {
+          // 1 / D of up to 2048 channels, a division each (some 80 cycles) spread over all threads; the two
+          // copies alternate, so one barrier per chunk also keeps the chunk before last's readers apart
+          float* rcp = rcp0 + turn * (kRcpBytes / 4);
+          turn ^= 1;
+          const int n = min(kRcpChunk, p.K - k0);
+#pragma unroll
+          for (int i = 0; i < kRcpChunk / kQuantThreads; ++i) {
+            const int c = tt + i * kQuantThreads;
+            rcp[(c >> 4) * kRcpStride + (c & 15)] = __frcp_rn(d0[i]);
+          }
+          if (k0 + kRcpChunk < p.K) load_d(g, k0 + kRcpChunk);
+          else if (g + 1 < g1) load_d(g + 1, 0);
+          __syncwarp();
+          ok = named_bar_all(2, kQuantThreads, ok);
+          if (!ok) break;
+          // half blocks over the threads, left-over threads on other rows; lanes without work repeat another's
+          const int HB = n / 16, split = kQuantThreads / HB;
+          const int rs = tt / HB, h = tt % HB, hb = k0 / 16 + h;
+          const int kt = hb >> 4, c = (hb >> 1) & 7;
+          float2 r2[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float4 v = __ldg(d + j);
-            r2[2 * j] = f2(__frcp_rn(v.x), __frcp_rn(v.y));
-            r2[2 * j + 1] = f2(__frcp_rn(v.z), __frcp_rn(v.w));
+            const float4 v = *reinterpret_cast<const float4*>(rcp + h * kRcpStride + 4 * j);
+            r2[2 * j] = f2(v.x, v.y);
+            r2[2 * j + 1] = f2(v.z, v.w);
           }
-        }
-        const int kt = hb >> 4, c = (hb >> 1) & 7;
-        for (int j0 = 0; j0 < rows; j0 += 2 * split) {  // two rows in flight
-          uint4 xv[2][2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int j = j0 + n * split + rs;
-            xv[n][0] = xv[n][1] = make_uint4(0, 0, 0, 0);
-            if (in && j < rows) {
-              const int64_t src = kDown ? ent[first + j] : ent_tok[first + j];
-              const uint4* s = reinterpret_cast<const uint4*>(p.a + src * p.K + hb * 16);
-              xv[n][0] = s[0];
-              xv[n][1] = s[1];
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int j = j0 + n * split + rs;
-            uint2 codes;
-            uint32_t scale;
-            act_half_block(xv[n], r2, upper, codes, scale);
-            if (in && j < rows) {
+          auto put = [&](int j, const uint2& codes, uint32_t scale) {
+            if (rs < split && j < rows) {
               *reinterpret_cast<uint2*>(bq + kt * kBCodeBytes + code_chunk_offset(j, c) + (upper ? 8 : 0)) = codes;
               if (!upper) bs[kt * kBSfBytes + (c >> 2) * 256 + j * 16 + (c & 3)] = static_cast<uint8_t>(scale);
             }
+          };
+          auto load = [&](int j, uint4 (&xv)[2]) {
+            const uint4* s =
+                reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(ent_tok[first + min(j, rows - 1)]) * p.K + hb * 16);
+            xv[0] = s[0];
+            xv[1] = s[1];
+          };
+          int j0 = 0;
+          for (; j0 + split < rows; j0 += 2 * split) {
+            uint4 xv[2][2];
+            uint2 codes[2];
+            uint32_t scale[2];
+            load(j0 + rs, xv[0]);
+            load(j0 + split + rs, xv[1]);
+            act_half_blocks<2>(xv, r2, upper, codes, scale);
+            put(j0 + rs, codes[0], scale[0]);
+            put(j0 + split + rs, codes[1], scale[1]);
+            __syncwarp();
+          }
+          if (j0 < rows) {
+            uint4 xv[1][2];
+            uint2 codes[1];
+            uint32_t scale[1];
+            load(j0 + rs, xv[0]);
+            act_half_blocks<1>(xv, r2, upper, codes, scale);
+            put(j0 + rs, codes[0], scale[0]);
+            __syncwarp();
           }
         }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bfull[buf]);
+        if (++buf == bufs) {
+          buf = 0;
+          buf_turn ^= 1;
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bfull[buf]);
     }
   }
   __syncwarp();
 
   if constexpr (kDown) {
-    // ---- sum of the cluster's tiles in rank order: task (token, 8 channels), dealt out to the ranks ----
+    // ---- sum of the cluster's tiles: task (token, 4 channels), dealt out to the ranks; each rank adds from its
+    // own tile on, round the cluster: an order that the sizes fix ----
     pdl_wait();  // y may still be read by an earlier kernel
     __syncthreads();
     cluster_sync_all();  // every CTA's tile is complete
     const uint32_t local = smem_u32(acc);
-    for (int task = static_cast<int>(threadIdx.x) * p.S + rank; task < p.T * 16; task += kThreads * p.S) {
-      const int t = task >> 4, c = (task & 15) * 8;
-      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int o = 0; o < p.S; ++o) {
-        const uint32_t at = mapa_shared(local + static_cast<uint32_t>((t * kRowsTile + c) * 4), static_cast<uint32_t>(o));
-        const float4 a = ld_dsmem_f32x4(at), b = ld_dsmem_f32x4(at + 16);
-        s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-        s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+    for (int task = static_cast<int>(threadIdx.x) * p.S + rank; task < p.T * 32; task += kThreads * p.S) {
+      const int t = task >> 5, c = (task & 31) * 4;
+      // all loads first, one round trip; from this CTA's own tile on, so that no CTA is read by all at once
+      float4 part[8];
+#pragma unroll
+      for (int o = 0; o < 8; ++o) {
+        if (o < p.S) {
+          const int from = rank + o < p.S ? rank + o : rank + o - p.S;
+          part[o] = ld_dsmem_f32x4(
+              mapa_shared(local + static_cast<uint32_t>((t * kRowsTile + c) * 4), static_cast<uint32_t>(from)));
+        }
       }
-      *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(t) * p.N + tile0 * kRowsTile + c) =
-          make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int o = 0; o < 8; ++o) {
+        if (o < p.S) {
+          s[0] += part[o].x; s[1] += part[o].y; s[2] += part[o].z; s[3] += part[o].w;
+        }
+      }
+      *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t) * p.N + tile0 * kRowsTile + c) =
+          make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
     }
     cluster_sync_all();  // no CTA leaves while another may still read its tile
   }

@@ -69,6 +69,17 @@ __device__ __forceinline__ uint32_t e2m1x8(float v0, float v1, float v2, float v
   return out;
 }
 
+// Two values -> one byte of E2M1 codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x2(float v0, float v1) {
+  uint32_t out;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "mov.b32 %0, {b, b, b, b};\n\t}"
+      : "=r"(out)
+      : "f"(v0), "f"(v1));
+  return out & 0xFFu;
+}
+
 // Reciprocals 1/D of one 256-wide K tile in shared memory: blocks 36 floats
 // apart, so each block starts on a 16-byte boundary and a warp's 16-byte loads of
 // the same element of the eight blocks cover all 32 banks once.

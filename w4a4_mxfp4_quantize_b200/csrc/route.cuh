@@ -1,11 +1,10 @@
 // Routing of a mixture-of-experts layer: the k largest logits of each token (ties to
 // the lowest index), their weights, and the (token, choice) pairs sorted by expert.
 //
-// A warp holds a token's logits as order-preserving 32-bit keys, key i of lane l
-// belonging to expert 32 i + l, and takes the largest k times: one warp-wide integer
-// maximum finds the value, one ballot (or, on a tie, one warp-wide minimum of the
-// indices) the expert.  Selection compares the logits themselves, so it is exact:
-// softmax and sigmoid are both increasing.  A NaN ranks as -infinity.
+// The lanes that share a token hold its logits as order-preserving 32-bit keys and take
+// the largest k times.  Logits are read past L1: in the layer's second kernel they may
+// have been written since this SM's L1 last saw them.  Selection compares the logits themselves, so it
+// is exact: softmax and sigmoid are both increasing.  A NaN ranks as -infinity.
 #pragma once
 #include <type_traits>
 
@@ -14,7 +13,7 @@
 
 namespace macaq {
 
-constexpr int kMaxChoices = 32;  // lane j of a warp ends up with choice j
+constexpr int kMaxChoices = 32;
 
 struct RouteRule {
   const void* logits;  // [T, E], bf16 or fp32
@@ -32,97 +31,204 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-// Logits are read past L1: in the layer's second kernel they may have been written
-// since this SM's L1 last saw them.
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return (key & 0x80000000u) ? __uint_as_float(key & 0x7FFFFFFFu) : __uint_as_float(~key);
+}
 __device__ __forceinline__ float load_logit(const RouteRule& r, int64_t at) {
   if (r.logits_f32) return __ldcg(static_cast<const float*>(r.logits) + at);
   return bf16lo(__ldcg(static_cast<const unsigned short*>(r.logits) + at));
 }
-__device__ __forceinline__ float warp_sum(float v) {
+
+// Reductions over the G lanes that share a token.
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) {
+    v = __reduce_max_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  }
+  return v;
+}
+template <int G, typename V>
+__device__ __forceinline__ V group_sum(V v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// One warp, one token: lane j < k receives choice j (the experts in falling order of
-// their logits) and its weight.  L: keys per lane, 32 L >= E.
+// A warp chooses for 32 / G tokens at a time, G lanes to a token, lane g of them holding
+// experts g L .. g L + L - 1 (G L >= E).  A round is a chain of steps that wait for one
+// another: local maximum, maximum of the lanes, removal of the largest.  One token over
+// 32 lanes takes 92 to 117 cycles a round (one warp-wide maximum instruction), four tokens
+// over 8 lanes each about 150 (three exchanges): the first where every warp has a token
+// at most, the second where there are more.
+template <int G_, int L_>
+struct Spread {
+  static constexpr int G = G_, L = L_, kTokens = 32 / G_, kSlots = 32 / G_;  // choices per lane: k <= 32
+};
+template <int kMaxE, typename F>
+__device__ __forceinline__ void for_spread(int E, bool few, F&& f) {
+  if (few && E <= 128) f(Spread<32, 4>());
+  else if (E <= 64) f(Spread<8, 8>());
+  else if (E <= 128) f(Spread<8, 16>());
+  else if (E <= 256) f(Spread<16, 16>());
+  else if (kMaxE <= 512 || E <= 512) f(Spread<32, 16>());
+  else f(Spread<32, 32>());
+}
+
+// One warp, up to kTokens tokens: token t0 + (lane / G) step.  Calls f(token, j, expert,
+// weight) for each choice j < k of each token below t1, from the lane that holds it.
+// `ids`: 32 kTokens words of shared memory of the warp's own.
 //   softmax: exp(l_j - max) / sum, over all E or (renorm) the chosen
 //   sigmoid: 1 / (1 + exp(-l_j)), divided (renorm) by the sum of the chosen
 // A logit of -infinity has weight zero, also where all are -infinity (a sigmoid
 // below 2^-126 is zero too).  A NaN logit makes the weights of its token NaN where
 // it is chosen or enters the sum.
-template <int L>
-__device__ __forceinline__ void choose_experts(const RouteRule& r, int64_t token, int& expert, float& weight) {
-  const int lane = threadIdx.x & 31;
-  const int64_t base = token * r.E;
+// A round takes every expert of the largest key.  Where that took more than k in the
+// end, or left the last round nothing, some were equal: the rounds run once more, one
+// expert a round, the lowest of the lowest lane.
+template <typename S, typename F>
+__device__ __forceinline__ void choose_experts(const RouteRule& r, int64_t t0, int64_t t1, int64_t step, int* ids, F&& f) {
+  constexpr int G = S::G, L = S::L;
+  const int lane = threadIdx.x & 31, g = lane % G, first = g * L;
+  const int64_t mine = t0 + (lane / G) * step;
+  const int64_t token = mine < t1 ? mine : t0;  // lanes without a token repeat the first
+  const int64_t base = token * r.E + first;
+  ids += lane / G * 32;
   uint32_t key[L];
   bool nan = false;
-  float v[L];
+  const bool vec = r.E % 4 == 0;  // rows and lanes start on four logits
+  if (r.logits_f32) {
+    const float* p = static_cast<const float*>(r.logits) + base;
+    if (vec) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) v[i] = i * 32 + lane < r.E ? load_logit(r, base + i * 32 + lane) : 0.f;
+      for (int i = 0; i < L; i += 4) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (first + i < r.E) v = __ldcg(reinterpret_cast<const float4*>(p + i));
+        key[i] = __float_as_uint(v.x);
+        key[i + 1] = __float_as_uint(v.y);
+        key[i + 2] = __float_as_uint(v.z);
+        key[i + 3] = __float_as_uint(v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < L; ++i) key[i] = first + i < r.E ? __float_as_uint(__ldcg(p + i)) : 0xFF800000u;
+    }
+  } else {
+    const unsigned short* p = static_cast<const unsigned short*>(r.logits) + base;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < L; i += 4) {
+        uint2 v = make_uint2(0xFF80FF80u, 0xFF80FF80u);
+        if (first + i < r.E) v = __ldcg(reinterpret_cast<const uint2*>(p + i));
+        key[i] = v.x << 16;
+        key[i + 1] = v.x & 0xFFFF0000u;
+        key[i + 2] = v.y << 16;
+        key[i + 3] = v.y & 0xFFFF0000u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < L; ++i) key[i] = first + i < r.E ? static_cast<uint32_t>(__ldcg(p + i)) << 16 : 0xFF800000u;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    key[i] = i * 32 + lane < r.E ? logit_key(v[i]) : 0u;
-    nan = nan || (i * 32 + lane < r.E && isnan(v[i]));
+    nan = nan || isnan(__uint_as_float(key[i]));
+    key[i] = first + i < r.E ? logit_key(__uint_as_float(key[i])) : 0u;
   }
-  uint32_t mine = 0;  // key of this lane's choice
-  float all = 0.f;    // softmax over all E: its sum
-  uint32_t top = 0;   // the largest key
-  expert = 0;
+  const uint32_t any_nan = __ballot_sync(0xffffffffu, nan) >> (lane / G * G);
+  nan = (any_nan & (0xffffffffu >> (32 - G))) != 0;  // of this token
+  auto local_max = [&] {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < L; ++i) m = max(m, key[i]);
+    return m;
+  };
+  float all = 0.f;  // softmax over all E: its sum
+  if (!r.sigmoid && !r.renorm) {
+    const float mx = key_logit(group_max<G>(local_max()));
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const float v = key_logit(key[i]);
+      all += key[i] == 0u || v == -INFINITY ? 0.f : __expf(v - mx);
+    }
+    all = group_sum<G>(all);
+    if (nan) all = __int_as_float(0x7FFFFFFF);
+  }
+  uint32_t chosen[S::kSlots];  // keys of choices g, g + G, ...
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i) chosen[i] = 0u;
+  uint32_t top = 0u, last = 0u;
+#pragma unroll 1
   for (int j = 0; j < r.k; ++j) {
-    uint32_t best = key[0];
+    const uint32_t m = group_max<G>(local_max());
+    int hit = -1;
 #pragma unroll
-    for (int i = 1; i < L; ++i) best = max(best, key[i]);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-    int at = 0;
+    for (int i = L - 1; i >= 0; --i) {
+      const bool take = key[i] == m;
+      hit = take ? first + i : hit;
+      key[i] = take ? 0u : key[i];
+    }
+    if (hit >= 0) ids[j] = hit;
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i)
-      if (key[i] == m) at = i;  // the lowest of this lane's
-    const uint32_t who = __ballot_sync(0xffffffffu, best == m);
-    uint32_t e;
-    if ((who & (who - 1)) == 0) e = static_cast<uint32_t>(__shfl_sync(0xffffffffu, at * 32 + lane, __ffs(who) - 1));
-    else e = __reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu);
-    if (j == 0) {
-      top = m;
-      if (!r.sigmoid && !r.renorm) {
-        const float mx = (m & 0x80000000u) ? __uint_as_float(m & 0x7FFFFFFFu) : __uint_as_float(~m);
-        float s = 0.f;
+    for (int i = 0; i < S::kSlots; ++i) chosen[i] = j == g + i * G ? m : chosen[i];
+    top = j == 0 ? m : top;
+    last = m;
+  }
+  int taken = 0;
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-          if (i * 32 + lane < r.E && v[i] != -INFINITY) s += __expf(v[i] - mx);
-        all = warp_sum(s);
+  for (int i = 0; i < L; ++i) taken += key[i] == 0u && first + i < r.E ? 1 : 0;
+  const bool again = group_sum<G>(taken) != r.k || last == 0u;
+  if (__any_sync(0xffffffffu, again)) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) key[i] = first + i < r.E ? logit_key(load_logit(r, base + i)) : 0u;
+#pragma unroll 1
+    for (int j = 0; j < r.k; ++j) {
+      const uint32_t best = local_max(), m = group_max<G>(best);
+      const uint32_t who = __ballot_sync(0xffffffffu, best == m) >> (lane / G * G);
+      bool own = g == __ffs(who) - 1;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        if (own && key[i] == m) {
+          ids[j] = first + i;
+          key[i] = 0u;
+          own = false;
+        }
       }
-    }
-    if (lane == j) {
-      expert = static_cast<int>(e);
-      mine = m;
-    }
+      __syncwarp();
 #pragma unroll
-    for (int i = 0; i < L; ++i)
-      if (i * 32 + lane == static_cast<int>(e)) key[i] = 0u;
+      for (int i = 0; i < S::kSlots; ++i) chosen[i] = j == g + i * G ? m : chosen[i];
+    }
   }
-  // the choice's own logit, NaN included (its key says -infinity)
-  float l = (mine & 0x80000000u) ? __uint_as_float(mine & 0x7FFFFFFFu) : __uint_as_float(~mine);
-  if (__any_sync(0xffffffffu, nan) && lane < r.k) l = load_logit(r, base + expert);
-  const float mx = (top & 0x80000000u) ? __uint_as_float(top & 0x7FFFFFFFu) : __uint_as_float(~top);
-  if (lane >= r.k || l == -INFINITY) weight = 0.f;  // also where the largest logit is -infinity itself
-  else if (r.sigmoid) weight = __fdividef(1.0f, 1.0f + __expf(-l));
-  else weight = __expf(l - mx);
+  __syncwarp();
+  const float mx = key_logit(top);
+  float w[S::kSlots], sum = 0.f;
+  int e[S::kSlots];
+#pragma unroll
+  for (int i = 0; i < S::kSlots; ++i) {
+    const bool in = g + i * G < r.k;
+    e[i] = in ? ids[g + i * G] : 0;
+    float l = key_logit(chosen[i]);
+    if (nan && in) {  // a NaN's key says -infinity
+      l = load_logit(r, token * r.E + e[i]);
+    }
+    const float x = __expf(r.sigmoid ? -l : l - mx);
+    w[i] = r.sigmoid ? __fdividef(1.0f, 1.0f + x) : x;
+    w[i] = !in || l == -INFINITY ? 0.f : w[i];  // also where the largest logit is -infinity itself
+    sum += w[i];
+  }
   if (r.renorm || !r.sigmoid) {
-    const float sum = r.renorm ? warp_sum(weight) : all;
-    weight = sum == 0.f ? 0.f : __fdividef(weight, sum);
+    sum = r.renorm ? group_sum<G>(sum) : all;
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i) w[i] = sum == 0.f ? 0.f : __fdividef(w[i], sum);
   }
-  weight *= r.scale;
-}
-
-template <typename F>
-__device__ __forceinline__ void for_keys_per_lane(int E, F&& f) {
-  if (E <= 32) f(std::integral_constant<int, 1>());
-  else if (E <= 64) f(std::integral_constant<int, 2>());
-  else if (E <= 128) f(std::integral_constant<int, 4>());
-  else if (E <= 256) f(std::integral_constant<int, 8>());
-  else if (E <= 512) f(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 32>());
+  if (mine < t1) {
+#pragma unroll
+    for (int i = 0; i < S::kSlots; ++i)
+      if (g + i * G < r.k) f(mine, g + i * G, e[i], w[i] * r.scale);
+  }
+  __syncwarp();  // `ids` may be written again
 }
 
 // ============================================================================
@@ -208,7 +314,8 @@ __device__ __forceinline__ void place_choices(const RouteParams& p, RouteTables&
 
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const __grid_constant__ RouteParams p) {
   __shared__ RouteTables s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int ids[kRouteThreads / 32 * 128];
+  const int warp = threadIdx.x >> 5;
   const int E = p.rule.E, k = p.rule.k;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.per_cta;
   const int64_t t1 = min(p.T, t0 + p.per_cta);
@@ -219,17 +326,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const __gri
   }
   pdl_wait();  // the logits may come from the kernel before
   pdl_trigger();
-  for_keys_per_lane(E, [&](auto keys) {
-    for (int64_t t = t0 + warp; t < t1; t += kRouteThreads / 32) {
-      int e;
-      float w;
-      choose_experts<decltype(keys)::value>(p.rule, t, e, w);
-      if (lane < k) {
-        p.ids[t * k + lane] = e;
-        p.weights[t * k + lane] = w;
+  for_spread<kRouteMaxE>(E, t1 - t0 <= kRouteThreads / 32, [&](auto spread) {
+    using S = decltype(spread);
+    for (int64_t t = t0 + warp * S::kTokens; t < t1; t += kRouteThreads / 32 * S::kTokens)
+      choose_experts<S>(p.rule, t, t1, 1, ids + warp * 128, [&](int64_t token, int j, int e, float w) {
+        p.ids[token * k + j] = e;
+        p.weights[token * k + j] = w;
         if (sorting) atomicAdd(&s.base[e], 1);
-      }
-    }
+      });
   });
   if (!sorting) return;
   __syncthreads();
