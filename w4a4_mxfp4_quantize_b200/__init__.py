@@ -651,8 +651,8 @@ def _element_type(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _shape(t, name: str, dtype, shape: tuple):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+def _shape(t: torch.Tensor, name: str, dtype, shape: tuple):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -660,45 +660,45 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-class _Place:
-    """The device and stream of a call: the first tensor's device (every other
-    tensor must be on it, contiguous), made current for the launch, and the given
-    stream or that device's current one.  Allocations are made on that stream."""
+def _place(stream, *ts):
+    """Where a call runs: every tensor contiguous on the first one's device (its index is
+    returned), and the context that makes that device and the stream current, None where
+    they are.  These calls take a few microseconds on the GPU: their checks are kept to
+    what costs a tenth of one."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("expected contiguous CUDA tensors on one device")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
+        return dev, torch.cuda.stream(stream)  # makes its device current too
+    return dev, None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
-    __slots__ = ("device", "stream", "_contexts")
 
-    def __init__(self, stream, *ts):
-        first = ts[0]
-        device = first.device
-        for t in ts:
-            if t is not None and (not t.is_cuda or not t.is_contiguous() or t.device != device):
-                raise ValueError("expected contiguous CUDA tensors on one device")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self.device, self.stream, self._contexts = device, stream, ()
+def _within(context, f, *args):
+    if context is None:
+        return f(*args)
+    with context:
+        return f(*args)
 
-    def __enter__(self):
-        if self.stream is not None:
-            self._contexts = (torch.cuda.stream(self.stream),)  # makes its device current too
-        elif torch.cuda.current_device() != self.device.index:
-            self._contexts = (torch.cuda.device(self.device),)
-        for c in self._contexts:
-            c.__enter__()
-        return self
 
-    def __exit__(self, *e):
-        for c in self._contexts:
-            c.__exit__(*e)
+def _scratch(nbytes: int, dev: int, given: torch.Tensor | None):
+    """Workspace of a call on the current stream.  A captured call gets memory of its own
+    from the graph's pool: two graphs never share it, and the kept buffer may be regrown."""
+    if nbytes == 0:
+        return None
+    if given is None:
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        buf = _ws.get((dev, _raw_stream(dev)))
+        if buf is not None and buf.numel() >= nbytes:
+            return buf
+    return workspace(nbytes, torch.device("cuda", dev), None, given)
 
-    def raw(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def scratch(self, nbytes: int, given: torch.Tensor | None):
-        """Workspace of a call.  A captured call gets memory of its own from the graph's
-        pool: two graphs never share it, and the kept buffer may be regrown later."""
-        if nbytes > 0 and given is None and torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return workspace(nbytes, self.device, self.stream, given)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty_strided  # the cheapest of torch's ways to new memory
 
 
 def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
@@ -714,14 +714,24 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Ten
     bf16 or fp32, [C] for one gate of all rows or [G, C] where row m takes gate row
     m // rows_per_gate (default 1: one per row)."""
     h_type = _element_type(h, "h")
-    if h.dim() != 2:
-        raise ValueError(f"h must have 2 dimensions, got shape {tuple(h.shape)}")
-    M, C = h.shape
-    _shape(y, "y", torch.bfloat16, (M, C))
-    _shape(w_post, "w_post", torch.float32, (C,))
-    _shape(w_pre, "w_pre", torch.float32, (C,))
-    _shape(out_h, "out_h", h.dtype, (M, C))
-    _shape(out_n, "out_n", torch.bfloat16, (M, C))
+    shape = h.shape
+    if len(shape) != 2:
+        raise ValueError(f"h must have 2 dimensions, got shape {tuple(shape)}")
+    M, C = shape
+    if y is not None:
+        _shape(y, "y", torch.bfloat16, (M, C))
+        if w_post is not None:
+            _shape(w_post, "w_post", torch.float32, (C,))
+    elif w_post is not None or gate is not None or out_h is not None:
+        raise ValueError("w_post, gate and out_h go with y")
+    if w_pre is not None:
+        _shape(w_pre, "w_pre", torch.float32, (C,))
+    elif out_n is not None:
+        raise ValueError("out_n goes with w_pre")
+    if out_h is not None:
+        _shape(out_h, "out_h", h.dtype, (M, C))
+    if out_n is not None:
+        _shape(out_n, "out_n", torch.bfloat16, (M, C))
     gate_type, per = 0, 1
     if gate is not None:
         gate_type = _element_type(gate, "gate")
@@ -735,17 +745,21 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Ten
                 raise ValueError(f"rows_per_gate must be at least 1, got {rows_per_gate}")
             want = (-(-M // per), C)
         _shape(gate, "gate", gate.dtype, want)
-    if y is None and (w_post is not None or gate is not None or out_h is not None):
-        raise ValueError("w_post, gate and out_h go with y")
-    if w_pre is None and out_n is not None:
-        raise ValueError("out_n goes with w_pre")
-    with _Place(stream, h, y, w_post, gate, w_pre, out_h, out_n) as at:
-        h_out = out_h if y is None or out_h is not None else torch.empty_like(h)
-        n = out_n if w_pre is None or out_n is not None else torch.empty((M, C), dtype=torch.bfloat16, device=h.device)
-        _check(lib().macaq_block_norm(_at(h), h_type, _at(y), _at(w_post), _at(gate), gate_type, per, _at(w_pre),
-                                      scale, eps, weight_offset, _at(h_out), _at(n), M, C, at.raw()),
-               "macaq_block_norm")
-    return (h if y is None else h_out), n
+    dev, context = _place(stream, h, y, w_post, gate, w_pre, out_h, out_n)
+    return _within(context, _block_norm, h, h_type, y, w_post, gate, gate_type, per, w_pre, scale, eps, weight_offset,
+                   out_h, out_n, M, C, dev)
+
+
+def _block_norm(h, h_type, y, w_post, gate, gate_type, per, w_pre, scale, eps, weight_offset, out_h, out_n, M, C, dev):
+    if y is not None and out_h is None:
+        out_h = torch.empty_like(h)
+    if w_pre is not None and out_n is None:
+        out_n = torch.empty_like(h, dtype=torch.bfloat16)
+    st = lib().macaq_block_norm(h.data_ptr(), h_type, _at(y), _at(w_post), _at(gate), gate_type, per, _at(w_pre),
+                                scale, eps, weight_offset, _at(out_h), _at(out_n), M, C, _raw_stream(dev))
+    if st:
+        raise MacaqError(st, "macaq_block_norm")
+    return (h if y is None else out_h), out_n
 
 
 def moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renorm: bool = True, scale: float = 1.0,
@@ -755,26 +769,31 @@ def moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renorm: 
     token order[r] // k, and counts is grouped_mm's group_list of type 1 for them.
     counts and order are None without sort."""
     logits_type = _element_type(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError(f"logits must have 2 dimensions, got shape {tuple(logits.shape)}")
-    T, E = logits.shape
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits must have 2 dimensions, got shape {tuple(shape)}")
+    T, E = shape
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be between 1 and min(E, 32) = {min(E, 32)}, got {k}")
+    dev, context = _place(stream, logits, ws)
+    return _within(context, _moe_route, logits, logits_type, T, E, k, score, renorm, scale, sort, ws, dev)
+
+
+def _moe_route(logits, logits_type, T, E, k, score, renorm, scale, sort, ws, dev):
     L = lib()
-    with _Place(stream, logits, ws) as at:
-        dev = logits.device
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        counts = order = None
-        need = 0
-        if sort:
-            counts = torch.empty(E, dtype=torch.int64, device=dev)
-            order = torch.empty(T * k, dtype=torch.int32, device=dev)
-            need = L.macaq_route_workspace_bytes(T, E)
-        ws = at.scratch(need, ws)
-        _check(L.macaq_moe_route(_at(logits), logits_type, T, E, k, score, bool(renorm), scale, _at(ids), _at(weights),
-                                 _at(counts), _at(order) if T else None, _at(ws), _nbytes(ws), at.raw()),
-               "macaq_moe_route")
+    device = logits.device
+    ids = _empty((T, k), (k, 1), dtype=torch.int32, device=device)
+    weights = torch.empty_like(ids, dtype=torch.float32)
+    counts = order = None
+    if sort:
+        counts = _empty((E,), (1,), dtype=torch.int64, device=device)
+        order = _empty((T * k,), (1,), dtype=torch.int32, device=device)
+        ws = _scratch(L.macaq_route_workspace_bytes(T, E), dev, ws)
+    st = L.macaq_moe_route(logits.data_ptr(), logits_type, T, E, k, score, 1 if renorm else 0, scale, ids.data_ptr(),
+                           weights.data_ptr(), _at(counts), _at(order) if T else None, _at(ws), _nbytes(ws),
+                           _raw_stream(dev))
+    if st:
+        raise MacaqError(st, "macaq_moe_route")
     return ids, weights, counts, order
 
 
@@ -790,14 +809,18 @@ def prepare_gate_up(W: torch.Tensor, D: torch.Tensor, stream=None) -> tuple[torc
     if N % 2:
         raise ValueError(f"W holds as many gate rows as up rows, got {N} rows")
     _shape(D, "D", torch.float32, (E, K))
+    dev, context = _place(stream, W, D)
+    return _within(context, _prepare_gate_up, W, D, E, N, K, dev)
+
+
+def _prepare_gate_up(W, D, E, N, K, dev):
     qb, sb = weight_bytes(E, N, K)
     if qb == 0:
         raise MacaqError(-3, "prepare_gate_up")
-    with _Place(stream, W, D) as at:
-        Wq = torch.empty(qb, dtype=torch.uint8, device=W.device)
-        Ws = torch.empty(sb, dtype=torch.uint8, device=W.device)
-        _check(lib().macaq_prepare_gate_up(_at(W), _at(D), E, N // 2, K, _at(Wq), _at(Ws), at.raw()),
-               "macaq_prepare_gate_up")
+    Wq = torch.empty(qb, dtype=torch.uint8, device=W.device)
+    Ws = torch.empty(sb, dtype=torch.uint8, device=W.device)
+    _check(lib().macaq_prepare_gate_up(_at(W), _at(D), E, N // 2, K, _at(Wq), _at(Ws), _raw_stream(dev)),
+           "macaq_prepare_gate_up")
     return Wq, Ws
 
 
@@ -822,16 +845,28 @@ def moe_mm(x: torch.Tensor, logits: torch.Tensor, D_up: torch.Tensor, Wq_up: tor
     E = logits.shape[1]
     _shape(D_up, "D_up", torch.float32, (E, H))
     _shape(D_down, "D_down", torch.float32, (E, inner))
-    _shape(out, "out", torch.bfloat16, (T, H))
+    if out is not None:
+        _shape(out, "out", torch.bfloat16, (T, H))
     _arg(status, "status", torch.int32, min_numel=1)
     L = lib()
-    for q, s, name, N, K in ((Wq_up, Ws_up, "up", 2 * inner, H), (Wq_down, Ws_down, "down", H, inner)):
-        _arg(q, "Wq_" + name, torch.uint8, min_numel=L.macaq_weight_code_bytes(E, N, K))
-        _arg(s, "Ws_" + name, torch.uint8, min_numel=L.macaq_weight_scale_bytes(E, N, K))
-    with _Place(stream, x, logits, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, out, status, ws) as at:
-        y = torch.empty_like(x) if out is None else out
-        ws = at.scratch(L.macaq_moe_workspace_bytes(T, k, inner), ws)
-        _check(L.macaq_moe_mm(_at(x), _at(logits), logits_type, _at(D_up), _at(Wq_up), _at(Ws_up), _at(D_down),
-                              _at(Wq_down), _at(Ws_down), T, E, k, H, inner, score, bool(renorm), scale, act_type,
-                              _at(y), _at(ws), _nbytes(ws), _at(status), at.raw()), "macaq_moe_mm")
+    _arg(Wq_up, "Wq_up", torch.uint8, min_numel=L.macaq_weight_code_bytes(E, 2 * inner, H))
+    _arg(Ws_up, "Ws_up", torch.uint8, min_numel=L.macaq_weight_scale_bytes(E, 2 * inner, H))
+    _arg(Wq_down, "Wq_down", torch.uint8, min_numel=L.macaq_weight_code_bytes(E, H, inner))
+    _arg(Ws_down, "Ws_down", torch.uint8, min_numel=L.macaq_weight_scale_bytes(E, H, inner))
+    dev, context = _place(stream, x, logits, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, out, status, ws)
+    return _within(context, _moe_mm, x, logits, logits_type, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, T, E, k, H,
+                   inner, score, renorm, scale, act_type, out, ws, status, dev)
+
+
+def _moe_mm(x, logits, logits_type, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, T, E, k, H, inner, score, renorm,
+            scale, act_type, out, ws, status, dev):
+    L = lib()
+    y = torch.empty_like(x) if out is None else out
+    ws = _scratch(L.macaq_moe_workspace_bytes(T, k, inner), dev, ws)
+    st = L.macaq_moe_mm(x.data_ptr(), logits.data_ptr(), logits_type, D_up.data_ptr(), Wq_up.data_ptr(),
+                        Ws_up.data_ptr(), D_down.data_ptr(), Wq_down.data_ptr(), Ws_down.data_ptr(), T, E, k, H, inner,
+                        score, 1 if renorm else 0, scale, act_type, y.data_ptr(), _at(ws), _nbytes(ws), _at(status),
+                        _raw_stream(dev))
+    if st:
+        raise MacaqError(st, "macaq_moe_mm")
     return y
