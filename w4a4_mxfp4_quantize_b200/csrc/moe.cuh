@@ -45,11 +45,7 @@ constexpr int kStageBytes = kTileCodeBytes + kTileSfBytes;
 constexpr int kTmemCols = 256;            // two accumulators of 16 columns, then 16 scale columns a stage
 constexpr int kSfCol = 32;
 constexpr int kBarBytes = 512;
-// up: reciprocals of D for 2048 channels at a time, half blocks 20 floats apart (lanes that
-// read 16 bytes of the same place in eight neighbouring half blocks meet no bank twice)
-constexpr int kRcpChunk = 2048;
-constexpr int kRcpStride = 20;
-constexpr int kRcpBytes = kRcpChunk / 16 * kRcpStride * 4;
+constexpr int kChunk = kQuantThreads * 8;  // up: channels that the quantiser takes at a time
 // up: an item's activations, 16 tokens x 64 channels of bf16, rows 144 bytes apart
 constexpr int kActStride = 72;
 constexpr int kActBytes = kRows * kActStride * 2;
@@ -65,7 +61,7 @@ __host__ __device__ inline int max_groups(int T, int k, int E) {
 }
 __host__ __device__ inline int align16i(int v) { return (v + 15) & ~15; }
 // Bytes of the tables that only choosing needs; they lie where the weight stages come later.
-__host__ __device__ inline int scratch_bytes(int T, int k, int E) { return align16i(T * k * 6) + E * 20 + kUpThreads / 32 * 512; }
+__host__ __device__ inline int scratch_bytes(int T, int k, int E) { return align16i(T * k * 6) + E * 20 + kUpThreads * 4; }
 __host__ inline Layout layout(int T, int k, int E, int K, bool down, int stages, int bufs) {
   const int KT = K / kKTile, tk = T * k, G = max_groups(T, k, E);
   Layout l;
@@ -79,8 +75,8 @@ __host__ inline Layout layout(int T, int k, int E, int K, bool down, int stages,
   l.ent_tok = l.ent + align16i(tk * 2);
   l.ent_w = l.ent_tok + align16i(tk * 2);
   l.grp = l.ent_w + align16i(tk * 4);
-  l.extra = l.grp + align16i(G * 8);  // down: the FP32 tile; up: activations and reciprocals
-  l.bytes = l.extra + (down ? T * kRowsTile * 4 : 2 * kActBytes + 2 * kRcpBytes) + 1024;
+  l.extra = l.grp + align16i(G * 8);  // down: the FP32 tile; up: activations
+  l.bytes = l.extra + (down ? T * kRowsTile * 4 : 2 * kActBytes) + 1024;
   return l;
 }
 }  // namespace moe
@@ -129,60 +125,51 @@ __device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t n, bool ok) 
 
 __device__ __forceinline__ float block_scale(uint32_t c) { return __uint_as_float((254u - min(c, 253u)) << 23); }
 
-// Half a 32-element activation block (16 bf16 values, their reciprocals of D) per lane,
-// lanes 2 i and 2 i + 1 together, R rows side by side: the arithmetic of act_block step
-// by step, its last butterfly stage (h = 16) and the block maximum exchanged between the
-// two lanes.
-template <int R>
-__device__ __forceinline__ void act_half_blocks(const uint4 (&xv)[R][2], const float2 (&r2)[8], bool upper,
-                                                uint2 (&codes)[R], uint32_t (&scale)[R]) {
-  float2 P[R][8];
+// A quarter of a 32-element activation block (8 bf16 values, their reciprocals of D) per
+// lane, four lanes to a block: the arithmetic of act_block step by step, its last two
+// butterfly stages (h = 8, 16) and the block maximum exchanged between the lanes.
+__device__ __forceinline__ void act_quarter_block(const uint4& xv, const float2 (&r2)[4], uint32_t& codes,
+                                                  uint32_t& scale) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t w[4] = {xv.x, xv.y, xv.z, xv.w};
+  float2 P[4];
 #pragma unroll
-  for (int n = 0; n < R; ++n) {
-    const uint32_t w[8] = {xv[n][0].x, xv[n][0].y, xv[n][0].z, xv[n][0].w,
-                           xv[n][1].x, xv[n][1].y, xv[n][1].z, xv[n][1].w};
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t xs = f2_to_bf16x2(f2_mul(bf16x2_to_f2(w[j]), r2[j]));
+    const float v0 = bf16lo(xs), v1 = bf16hi(xs);
+    P[j] = f2(__fadd_rn(v0, v1), __fsub_rn(v0, v1));
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t xs = f2_to_bf16x2(f2_mul(bf16x2_to_f2(w[j]), r2[j]));
-      const float v0 = bf16lo(xs), v1 = bf16hi(xs);
-      P[n][j] = f2(__fadd_rn(v0, v1), __fsub_rn(v0, v1));
-    }
+  for (int hp = 1; hp < 4; hp <<= 1) {
 #pragma unroll
-    for (int hp = 1; hp < 8; hp <<= 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i & hp) continue;
-        const float2 a = P[n][i], b = P[n][i + hp];
-        P[n][i] = f2_add(a, b);
-        P[n][i + hp] = f2_sub(a, b);
-      }
+    for (int i = 0; i < 4; ++i) {
+      if (i & hp) continue;
+      const float2 a = P[i], b = P[i + hp];
+      P[i] = f2_add(a, b);
+      P[i + hp] = f2_sub(a, b);
     }
   }
-  const float sign = upper ? -1.0f : 1.0f;  // lower lane: mine + other, upper lane: other - mine
-  const float2 s2 = f2(sign, sign);
-  float2 o[R][8];
 #pragma unroll
-  for (int n = 0; n < R; ++n)
+  for (int h = 1; h < 4; h <<= 1) {
+    // lower lane: mine + other, upper lane: other - mine; the product by +-1 is exact: one rounding
+    const float sign = (lane & h) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      o[n][j] = f2(__shfl_xor_sync(0xffffffffu, P[n][j].x, 1), __shfl_xor_sync(0xffffffffu, P[n][j].y, 1));
-#pragma unroll
-  for (int n = 0; n < R; ++n) {
-    uint32_t u[8], m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      u[j] = f2_to_bf16x2(ffma2(P[n][j], s2, o[n][j]));  // the product by +-1 is exact: one rounding
-      m = max_u16x2(m, u[j] & 0x7FFF7FFFu);
-    }
-    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t c = e8m0_from_amax_bits(max(m & 0xFFFFu, m >> 16) << 16);
-    const float2 q2 = f2(block_scale(c), block_scale(c));
-    codes[n].x = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[0]), q2), f2_mul(bf16x2_to_f2(u[1]), q2),
-                           f2_mul(bf16x2_to_f2(u[2]), q2), f2_mul(bf16x2_to_f2(u[3]), q2));
-    codes[n].y = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[4]), q2), f2_mul(bf16x2_to_f2(u[5]), q2),
-                           f2_mul(bf16x2_to_f2(u[6]), q2), f2_mul(bf16x2_to_f2(u[7]), q2));
-    scale[n] = c;
+    for (int j = 0; j < 4; ++j)
+      P[j] = ffma2(P[j], f2(sign, sign),
+                   f2(__shfl_xor_sync(0xffffffffu, P[j].x, h), __shfl_xor_sync(0xffffffffu, P[j].y, h)));
   }
+  uint32_t u[4], m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    u[j] = f2_to_bf16x2(P[j]);
+    m = max_u16x2(m, u[j] & 0x7FFF7FFFu);
+  }
+  m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  scale = e8m0_from_amax_bits(max(m & 0xFFFFu, m >> 16) << 16);
+  const float2 q2 = f2(block_scale(scale), block_scale(scale));
+  codes = e2m1x8_f2(f2_mul(bf16x2_to_f2(u[0]), q2), f2_mul(bf16x2_to_f2(u[1]), q2), f2_mul(bf16x2_to_f2(u[2]), q2),
+                    f2_mul(bf16x2_to_f2(u[3]), q2));
 }
 
 // One 32-element block per warp, element `lane` of R rows: the same steps with every
@@ -211,9 +198,12 @@ __device__ __forceinline__ void act_lane_blocks(const float (&x)[R], float r, ui
 }
 
 // A load that is issued where it stands, before the barrier that lets the weights follow.
-__device__ __forceinline__ float ld_now(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+__device__ __forceinline__ float4 ld_now(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
 }
 
@@ -231,24 +221,21 @@ __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uin
   uint16_t* sel_e = reinterpret_cast<uint16_t*>(sel_w + tk);
   uint32_t* mask = reinterpret_cast<uint32_t*>(scratch + moe::align16i(tk * 6));  // [E][4]: tokens that chose e
   int* off = reinterpret_cast<int*>(mask + E * 4);                                // [E]: first entry
-  int* ids = off + E;                                                             // [kWarps][128]
+  int* ids = off + E;                                                             // [kWarps][32]
   uint16_t* ent = reinterpret_cast<uint16_t*>(smem + p.l.ent);
   uint16_t* ent_tok = reinterpret_cast<uint16_t*>(smem + p.l.ent_tok);
   float* ent_w = reinterpret_cast<float*>(smem + p.l.ent_w);
   int2* grp = reinterpret_cast<int2*>(smem + p.l.grp);
   for (int i = threadIdx.x; i < E * 4; i += kThreads) mask[i] = 0u;
   __syncthreads();
-  for_spread<moe::kMaxExperts>(E, T <= kWarps, [&](auto spread) {
-    using S = decltype(spread);
-    // tokens warp, warp + kWarps, ...: few tokens are spread over the warps before they share one
-    for (int t = warp; t < T; t += kWarps * S::kTokens)
-      choose_experts<S>(p.rule, t, T, kWarps, ids + warp * 128, [&](int64_t tok, int j, int e, float w) {
-        const int at = static_cast<int>(tok) * k + j;
-        const bool used = w != 0.f;
-        sel_w[at] = w;
-        sel_e[at] = used ? static_cast<uint16_t>(e) : 0xFFFFu;
-        if (used) atomicOr(&mask[e * 4 + (static_cast<int>(tok) >> 5)], 1u << (tok & 31));
-      });
+  choose_all<moe::kMaxExperts>(p.rule, warp, T, kWarps, ids + warp * 32, [&](int64_t token, int e, float w) {
+    if (lane < k) {
+      const int t = static_cast<int>(token);
+      const bool used = w != 0.f;
+      sel_w[t * k + lane] = w;
+      sel_e[t * k + lane] = used ? static_cast<uint16_t>(e) : 0xFFFFu;
+      if (used) atomicOr(&mask[e * 4 + (t >> 5)], 1u << (t & 31));
+    }
   });
   __syncthreads();
   // entries and groups before each expert, one expert per thread
@@ -582,49 +569,61 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
       if constexpr (!kDown) rcp = __frcp_rn(__ldg(p.D_next + static_cast<int64_t>(e) * (p.N / 2) + channel));
       __syncwarp();
       const bool ok = mbar_wait_warp(&accf[ab], (w.i >> 1) & 1, abort_flag, kWaitTimeoutNs);
-      uint32_t r[kRows];
-      if (ok) {
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * kRows;
+      if constexpr (kDown) {
+        if (!ok) break;
         tc_fence_after();
-        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + ab * kRows, r);
-        tmem_wait_ld();
+#pragma unroll 1
+        for (int j0 = 0; j0 < rows; j0 += 4) {
+          uint32_t r[4];
+          tmem_ld_32x32b_x4(taddr + j0, r);
+          // the tokens of a group differ, so their sums are read together, then written
+          float* o[4];
+          float wt[4], v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int jj = first + min(j0 + j, rows - 1);
+            o[j] = acc + ent_tok[jj] * kRowsTile + row;
+            wt[j] = ent_w[jj] * 0.03125f;
+            v[j] = *o[j];
+          }
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j0 + j < rows) *o[j] = fmaf(wt[j], __uint_as_float(r[j]), v[j]);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acce[ab]);
-      }
-      if constexpr (kDown) {
-        if (!ok) break;
-        // the tokens of a group differ, so their sums are read together, then written
-        float* o[kRows];
-        float v[kRows];
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          const int jj = first + min(j, rows - 1);
-          o[j] = acc + ent_tok[jj] * kRowsTile + row;
-          v[j] = fmaf(ent_w[jj] * 0.03125f, __uint_as_float(r[j]), *o[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kRows; ++j)
-          if (j < rows) *o[j] = v[j];
       } else {
         // weight rows 2 c and 2 c + 1 are the gate and the up row of channel c: of two tokens
         // the even lane finishes the first, the odd lane the second
         uint16_t* act = reinterpret_cast<uint16_t*>(smem + p.l.extra + ab * kActBytes);
         if (ok) {
+          tc_fence_after();
           const bool odd = lane & 1;
+#pragma unroll 1
+          for (int j0 = 0; j0 < rows; j0 += 4) {
+            uint32_t r[4];
+            tmem_ld_32x32b_x4(taddr + j0, r);
+            tmem_wait_ld(r);
 #pragma unroll
-          for (int j = 0; j < kRows; j += 2) {
-            if (j < rows) {
+            for (int j = 0; j < 4; j += 2) {
               const float a = __uint_as_float(r[j]) * 0.03125f, b = __uint_as_float(r[j + 1]) * 0.03125f;
               const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-              act[(j + (odd ? 1 : 0)) * kActStride + (row >> 1)] =
+              act[(j0 + j + (odd ? 1 : 0)) * kActStride + (row >> 1)] =
                   bf16_bits(gated(odd ? other : a, odd ? b : other, p.gelu));
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acce[ab]);
         }
         // (the two copies of `act` alternate: this barrier also separates an item's reads from
         // the writes of the item after the next)
         if (!named_bar_all(1, 128, ok)) break;
         const uint16_t* mine = act + (q >> 1) * 32 + lane;
+#pragma unroll 1
         for (int j = q & 1; j < rows; j += 4) {  // tokens j and j + 2
           const int j2 = min(j + 2, rows - 1);
           const float h[2] = {bf16lo(mine[j * kActStride]), bf16lo(mine[j2 * kActStride])};
@@ -644,25 +643,20 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
     }
   } else {
     if constexpr (!kDown) {
-      // ---- x quantiser: all of its warps on one group after the other ----
+      // ---- x quantiser: all of its warps on one group after the other.  A thread owns eight channels of a
+      // chunk of 2048, so their reciprocals stay in its registers; threads left over take other rows ----
       const int tt = static_cast<int>(threadIdx.x) - 8 * 32;
-      const bool upper = lane & 1;
-      float* rcp0 = reinterpret_cast<float*>(smem + p.l.extra + 2 * kActBytes);
-      int turn = 0;
-      bool ok = true;
-      // the channel factors of a group's first chunk are loaded a group ahead
-      float d0[kRcpChunk / kQuantThreads];
+      // the channel factors of the next chunk (of this group or the next) are loaded ahead
+      float4 d[2];
       auto load_d = [&](int g, int k0) {
-        const float* d = p.D + static_cast<int64_t>(grp[g].y & 0xFFFF) * p.K + k0;
-#pragma unroll
-        for (int i = 0; i < kRcpChunk / kQuantThreads; ++i) {
-          const int c = tt + i * kQuantThreads;
-          d0[i] = 1.0f;
-          if (k0 + c < p.K) d0[i] = ld_now(d + c);
-        }
+        const int ch = min(k0 + tt % (min(kChunk, p.K - k0) / 8) * 8, p.K - 8);
+        const float* src = p.D + static_cast<int64_t>(grp[g].y & 0xFFFF) * p.K + ch;
+        d[0] = ld_now(src);
+        d[1] = ld_now(src + 4);
       };
       if (g0 < g1) load_d(g0, 0);
       asm volatile("bar.arrive 3, %0;" ::"n"(kQuantThreads + 32) : "memory");
+      bool ok = true;
       int buf = 0;
       uint32_t buf_turn = 1;
       for (int g = g0; g < g1 && ok; ++g) {
@@ -671,68 +665,37 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
         uint8_t* bq = smem + p.l.b + buf * KT * kBCodeBytes;
         uint8_t* bs = smem + p.l.bsf + buf * KT * kBSfBytes;
         ok = mbar_wait_warp(&bempty[buf], buf_turn, abort_flag, kWaitTimeoutNs);
-        for (int k0 = 0; k0 < p.K; k0 += kRcpChunk) {
-          // 1 / D of up to 2048 channels, a division each (some 80 cycles) spread over all threads; the two
-          // copies alternate, so one barrier per chunk also keeps the chunk before last's readers apart
-          float* rcp = rcp0 + turn * (kRcpBytes / 4);
-          turn ^= 1;
-          const int n = min(kRcpChunk, p.K - k0);
-#pragma unroll
-          for (int i = 0; i < kRcpChunk / kQuantThreads; ++i) {
-            const int c = tt + i * kQuantThreads;
-            rcp[(c >> 4) * kRcpStride + (c & 15)] = __frcp_rn(d0[i]);
-          }
-          if (k0 + kRcpChunk < p.K) load_d(g, k0 + kRcpChunk);
+        if (!ok) break;
+#pragma unroll 1
+        for (int k0 = 0; k0 < p.K; k0 += kChunk) {
+          const int pieces = min(kChunk, p.K - k0) / 8, split = kQuantThreads / pieces;
+          const int rs = tt / pieces, ch = k0 + tt % pieces * 8;
+          const int kt = ch >> 8, c = (ch >> 5) & 7;
+          const float2 r2[4] = {f2(__frcp_rn(d[0].x), __frcp_rn(d[0].y)), f2(__frcp_rn(d[0].z), __frcp_rn(d[0].w)),
+                                f2(__frcp_rn(d[1].x), __frcp_rn(d[1].y)), f2(__frcp_rn(d[1].z), __frcp_rn(d[1].w))};
+          if (k0 + kChunk < p.K) load_d(g, k0 + kChunk);
           else if (g + 1 < g1) load_d(g + 1, 0);
-          __syncwarp();
-          ok = named_bar_all(2, kQuantThreads, ok);
-          if (!ok) break;
-          // half blocks over the threads, left-over threads on other rows; lanes without work repeat another's
-          const int HB = n / 16, split = kQuantThreads / HB;
-          const int rs = tt / HB, h = tt % HB, hb = k0 / 16 + h;
-          const int kt = hb >> 4, c = (hb >> 1) & 7;
-          float2 r2[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(rcp + h * kRcpStride + 4 * j);
-            r2[2 * j] = f2(v.x, v.y);
-            r2[2 * j + 1] = f2(v.z, v.w);
-          }
-          auto put = [&](int j, const uint2& codes, uint32_t scale) {
-            if (rs < split && j < rows) {
-              *reinterpret_cast<uint2*>(bq + kt * kBCodeBytes + code_chunk_offset(j, c) + (upper ? 8 : 0)) = codes;
-              if (!upper) bs[kt * kBSfBytes + (c >> 2) * 256 + j * 16 + (c & 3)] = static_cast<uint8_t>(scale);
-            }
+          const uint16_t* x = p.x + ch;
+          // lanes without a row repeat the last one and store nothing
+          auto load_x = [&](int j) {
+            return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(ent_tok[first + min(j, rows - 1)]) * p.K);
           };
-          auto load = [&](int j, uint4 (&xv)[2]) {
-            const uint4* s =
-                reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(ent_tok[first + min(j, rows - 1)]) * p.K + hb * 16);
-            xv[0] = s[0];
-            xv[1] = s[1];
-          };
-          int j0 = 0;
-          for (; j0 + split < rows; j0 += 2 * split) {
-            uint4 xv[2][2];
-            uint2 codes[2];
-            uint32_t scale[2];
-            load(j0 + rs, xv[0]);
-            load(j0 + split + rs, xv[1]);
-            act_half_blocks<2>(xv, r2, upper, codes, scale);
-            put(j0 + rs, codes[0], scale[0]);
-            put(j0 + split + rs, codes[1], scale[1]);
+          uint4 next = load_x(rs);
+#pragma unroll 1
+          for (int j0 = 0; j0 < rows; j0 += split) {
+            const uint4 xv = next;
+            const int j = j0 + rs;
+            next = load_x(j + split);
             __syncwarp();
-          }
-          if (j0 < rows) {
-            uint4 xv[1][2];
-            uint2 codes[1];
-            uint32_t scale[1];
-            load(j0 + rs, xv[0]);
-            act_half_blocks<1>(xv, r2, upper, codes, scale);
-            put(j0 + rs, codes[0], scale[0]);
+            uint32_t codes, scale;
+            act_quarter_block(xv, r2, codes, scale);
+            if (rs < split && j < rows) {
+              *reinterpret_cast<uint32_t*>(bq + kt * kBCodeBytes + code_chunk_offset(j, c) + (lane & 3) * 4) = codes;
+              if ((lane & 3) == 0) bs[kt * kBSfBytes + (c >> 2) * 256 + j * 16 + (c & 3)] = static_cast<uint8_t>(scale);
+            }
             __syncwarp();
           }
         }
-        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bfull[buf]);

@@ -1,8 +1,8 @@
 // Routing of a mixture-of-experts layer: the k largest logits of each token (ties to
 // the lowest index), their weights, and the (token, choice) pairs sorted by expert.
 //
-// The lanes that share a token hold its logits as order-preserving 32-bit keys and take
-// the largest k times.  Logits are read past L1: in the layer's second kernel they may
+// A warp holds a token's logits as order-preserving 32-bit keys and takes the largest k
+// times.  Logits are read past L1: in the layer's second kernel they may
 // have been written since this SM's L1 last saw them.  Selection compares the logits themselves, so it
 // is exact: softmax and sigmoid are both increasing.  A NaN ranks as -infinity.
 #pragma once
@@ -27,9 +27,8 @@ struct RouteRule {
 // Order-preserving unsigned key of a logit; -0 counts as +0 and NaN as -infinity.
 // No logit has key 0: it marks an expert that is taken (or past E).
 __device__ __forceinline__ uint32_t logit_key(float v) {
-  if (isnan(v)) v = -INFINITY;
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(v, -INFINITY) + 0.0f);  // the maximum of a NaN and a number is the number
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
   return (key & 0x80000000u) ? __uint_as_float(key & 0x7FFFFFFFu) : __uint_as_float(~key);
@@ -39,196 +38,187 @@ __device__ __forceinline__ float load_logit(const RouteRule& r, int64_t at) {
   return bf16lo(__ldcg(static_cast<const unsigned short*>(r.logits) + at));
 }
 
-// Reductions over the G lanes that share a token.
-template <int G>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  if constexpr (G == 32) {
-    v = __reduce_max_sync(0xffffffffu, v);
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int kMaxE, typename F>
+__device__ __forceinline__ void for_keys_per_lane(int E, F&& f) {
+  if (E <= 64) f(std::integral_constant<int, 2>());
+  else if (E <= 128) f(std::integral_constant<int, 4>());
+  else if (E <= 256) f(std::integral_constant<int, 8>());
+  else if (kMaxE <= 512 || E <= 512) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 32>());
+}
+
+// A token's logits, lane l the experts l L .. l L + L - 1 (32 L >= E).
+template <int L, bool kBf16>
+__device__ __forceinline__ void load_logits(const RouteRule& r, int64_t token, float (&v)[L]) {
+  const int first = (threadIdx.x & 31) * L;
+  const int64_t base = token * r.E + first;
+  if (L % 4 == 0 && r.E % 4 == 0) {  // rows and lanes start on four logits
+#pragma unroll
+    for (int i = 0; i < L; i += 4) {
+      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (first + i < r.E) {
+        if constexpr (kBf16) {
+          const uint2 w = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(r.logits) + base + i));
+          x = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+        } else {
+          x = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(r.logits) + base + i));
+        }
+      }
+      v[i] = x.x;
+      if constexpr (L % 4 == 0) {
+        v[i + 1] = x.y;
+        v[i + 2] = x.z;
+        v[i + 3] = x.w;
+      }
+    }
   } else {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int i = 0; i < L; ++i) {
+      v[i] = -INFINITY;
+      if (first + i < r.E)
+        v[i] = kBf16 ? bf16lo(__ldcg(static_cast<const unsigned short*>(r.logits) + base + i))
+                     : __ldcg(static_cast<const float*>(r.logits) + base + i);
+    }
   }
-  return v;
-}
-template <int G, typename V>
-__device__ __forceinline__ V group_sum(V v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
 }
 
-// A warp chooses for 32 / G tokens at a time, G lanes to a token, lane g of them holding
-// experts g L .. g L + L - 1 (G L >= E).  A round is a chain of steps that wait for one
-// another: local maximum, maximum of the lanes, removal of the largest.  One token over
-// 32 lanes takes 92 to 117 cycles a round (one warp-wide maximum instruction), four tokens
-// over 8 lanes each about 150 (three exchanges): the first where every warp has a token
-// at most, the second where there are more.
-template <int G_, int L_>
-struct Spread {
-  static constexpr int G = G_, L = L_, kTokens = 32 / G_, kSlots = 32 / G_;  // choices per lane: k <= 32
-};
-template <int kMaxE, typename F>
-__device__ __forceinline__ void for_spread(int E, bool few, F&& f) {
-  if (few && E <= 128) f(Spread<32, 4>());
-  else if (E <= 64) f(Spread<8, 8>());
-  else if (E <= 128) f(Spread<8, 16>());
-  else if (E <= 256) f(Spread<16, 16>());
-  else if (kMaxE <= 512 || E <= 512) f(Spread<32, 16>());
-  else f(Spread<32, 32>());
-}
-
-// One warp, up to kTokens tokens: token t0 + (lane / G) step.  Calls f(token, j, expert,
-// weight) for each choice j < k of each token below t1, from the lane that holds it.
-// `ids`: 32 kTokens words of shared memory of the warp's own.
+// One warp, one token: returns this lane's choice (j = lane < k) and its weight, from the
+// logits of load_logits.  `ids`: 32 words of shared memory of the warp's own.
 //   softmax: exp(l_j - max) / sum, over all E or (renorm) the chosen
 //   sigmoid: 1 / (1 + exp(-l_j)), divided (renorm) by the sum of the chosen
 // A logit of -infinity has weight zero, also where all are -infinity (a sigmoid
 // below 2^-126 is zero too).  A NaN logit makes the weights of its token NaN where
 // it is chosen or enters the sum.
-// A round takes every expert of the largest key.  Where that took more than k in the
-// end, or left the last round nothing, some were equal: the rounds run once more, one
-// expert a round, the lowest of the lowest lane.
-template <typename S, typename F>
-__device__ __forceinline__ void choose_experts(const RouteRule& r, int64_t t0, int64_t t1, int64_t step, int* ids, F&& f) {
-  constexpr int G = S::G, L = S::L;
-  const int lane = threadIdx.x & 31, g = lane % G, first = g * L;
-  const int64_t mine = t0 + (lane / G) * step;
-  const int64_t token = mine < t1 ? mine : t0;  // lanes without a token repeat the first
-  const int64_t base = token * r.E + first;
-  ids += lane / G * 32;
+// A round is a chain of steps that wait for one another (the lane's maximum, the warp's,
+// the removal: 92 cycles at L = 4).  kPacked (bf16 logits): the key's upper half is the
+// logit, the lower the expert, higher for a lower index, so keys differ and say which
+// expert they are.  Else (fp32) a round takes every expert of the largest key; where that
+// took more than k in the end, or left the last round nothing, some were equal and the
+// rounds run once more, one expert a round, the lowest of the lowest lane.
+// The code is kept short: a kernel of a few microseconds reads it once, from L2 (four
+// tokens to a warp, eight lanes each, in four times the instructions, took as long).
+template <int L, bool kPacked>
+__device__ __forceinline__ void choose_experts(const RouteRule& r, int64_t token, const float (&v)[L], int* ids,
+                                               int& expert, float& weight) {
+  const int lane = threadIdx.x & 31, first = lane * L;
   uint32_t key[L];
-  bool nan = false;
-  const bool vec = r.E % 4 == 0;  // rows and lanes start on four logits
-  if (r.logits_f32) {
-    const float* p = static_cast<const float*>(r.logits) + base;
-    if (vec) {
+  auto make_keys = [&] {
 #pragma unroll
-      for (int i = 0; i < L; i += 4) {
-        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (first + i < r.E) v = __ldcg(reinterpret_cast<const float4*>(p + i));
-        key[i] = __float_as_uint(v.x);
-        key[i + 1] = __float_as_uint(v.y);
-        key[i + 2] = __float_as_uint(v.z);
-        key[i + 3] = __float_as_uint(v.w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < L; ++i) key[i] = first + i < r.E ? __float_as_uint(__ldcg(p + i)) : 0xFF800000u;
+    for (int i = 0; i < L; ++i) {
+      uint32_t u = logit_key(v[i]);
+      if constexpr (kPacked) u = (u & 0xFFFF0000u) | static_cast<uint32_t>(0xFFFF - (first + i));
+      key[i] = first + i < r.E ? u : 0u;
     }
-  } else {
-    const unsigned short* p = static_cast<const unsigned short*>(r.logits) + base;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < L; i += 4) {
-        uint2 v = make_uint2(0xFF80FF80u, 0xFF80FF80u);
-        if (first + i < r.E) v = __ldcg(reinterpret_cast<const uint2*>(p + i));
-        key[i] = v.x << 16;
-        key[i + 1] = v.x & 0xFFFF0000u;
-        key[i + 2] = v.y << 16;
-        key[i + 3] = v.y & 0xFFFF0000u;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < L; ++i) key[i] = first + i < r.E ? static_cast<uint32_t>(__ldcg(p + i)) << 16 : 0xFF800000u;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    nan = nan || isnan(__uint_as_float(key[i]));
-    key[i] = first + i < r.E ? logit_key(__uint_as_float(key[i])) : 0u;
-  }
-  const uint32_t any_nan = __ballot_sync(0xffffffffu, nan) >> (lane / G * G);
-  nan = (any_nan & (0xffffffffu >> (32 - G))) != 0;  // of this token
+  };
   auto local_max = [&] {
     uint32_t m = key[0];
 #pragma unroll
     for (int i = 1; i < L; ++i) m = max(m, key[i]);
     return m;
   };
-  float all = 0.f;  // softmax over all E: its sum
-  if (!r.sigmoid && !r.renorm) {
-    const float mx = key_logit(group_max<G>(local_max()));
+  make_keys();
+  float any = v[0];
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const float v = key_logit(key[i]);
-      all += key[i] == 0u || v == -INFINITY ? 0.f : __expf(v - mx);
-    }
-    all = group_sum<G>(all);
-    if (nan) all = __int_as_float(0x7FFFFFFF);
-  }
-  uint32_t chosen[S::kSlots];  // keys of choices g, g + G, ...
-#pragma unroll
-  for (int i = 0; i < S::kSlots; ++i) chosen[i] = 0u;
-  uint32_t top = 0u, last = 0u;
+  for (int i = 1; i < L; ++i) any += v[i];
+  const bool nan = __any_sync(0xffffffffu, isnan(any));  // a NaN (or infinities of both signs: no harm)
+  uint32_t mine = 0u, m = 0u;  // the keys of this lane's choice and of the round's
 #pragma unroll 1
   for (int j = 0; j < r.k; ++j) {
-    const uint32_t m = group_max<G>(local_max());
-    int hit = -1;
+    m = __reduce_max_sync(0xffffffffu, local_max());
+    mine = lane == j ? m : mine;
+    if constexpr (kPacked) {
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-      const bool take = key[i] == m;
-      hit = take ? first + i : hit;
-      key[i] = take ? 0u : key[i];
-    }
-    if (hit >= 0) ids[j] = hit;
-#pragma unroll
-    for (int i = 0; i < S::kSlots; ++i) chosen[i] = j == g + i * G ? m : chosen[i];
-    top = j == 0 ? m : top;
-    last = m;
-  }
-  int taken = 0;
-#pragma unroll
-  for (int i = 0; i < L; ++i) taken += key[i] == 0u && first + i < r.E ? 1 : 0;
-  const bool again = group_sum<G>(taken) != r.k || last == 0u;
-  if (__any_sync(0xffffffffu, again)) {
-#pragma unroll
-    for (int i = 0; i < L; ++i) key[i] = first + i < r.E ? logit_key(load_logit(r, base + i)) : 0u;
-#pragma unroll 1
-    for (int j = 0; j < r.k; ++j) {
-      const uint32_t best = local_max(), m = group_max<G>(best);
-      const uint32_t who = __ballot_sync(0xffffffffu, best == m) >> (lane / G * G);
-      bool own = g == __ffs(who) - 1;
+      for (int i = 0; i < L; ++i) key[i] = key[i] == m ? 0u : key[i];
+    } else {
+      int hit = -1;
 #pragma unroll
       for (int i = 0; i < L; ++i) {
-        if (own && key[i] == m) {
-          ids[j] = first + i;
-          key[i] = 0u;
-          own = false;
+        const bool take = key[i] == m;
+        hit = take ? first + i : hit;
+        key[i] = take ? 0u : key[i];
+      }
+      if (hit >= 0) ids[j] = hit;
+    }
+  }
+  if constexpr (kPacked) {
+    expert = lane < r.k ? 0xFFFF - static_cast<int>(mine & 0xFFFFu) : 0;
+    // the logit's key again: the bits below bf16 are those of a value whose low half is zero
+    mine = (mine & 0x80000000u) ? mine & 0xFFFF0000u : mine | 0xFFFFu;
+  } else {
+    uint32_t taken = 0u;  // how many of this lane's experts are gone
+#pragma unroll
+    for (int i = 0; i < L; ++i) taken += key[i] == 0u && first + i < r.E ? 1u : 0u;
+    if (__reduce_add_sync(0xffffffffu, taken) != static_cast<uint32_t>(r.k) || m == 0u) {
+      make_keys();
+#pragma unroll 1
+      for (int j = 0; j < r.k; ++j) {
+        const uint32_t best = local_max();
+        m = __reduce_max_sync(0xffffffffu, best);
+        mine = lane == j ? m : mine;
+        bool own = lane == __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          if (own && key[i] == m) {
+            ids[j] = first + i;
+            key[i] = 0u;
+            own = false;
+          }
         }
       }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < S::kSlots; ++i) chosen[i] = j == g + i * G ? m : chosen[i];
     }
+    __syncwarp();
+    expert = lane < r.k ? ids[lane] : 0;
   }
-  __syncwarp();
-  const float mx = key_logit(top);
-  float w[S::kSlots], sum = 0.f;
-  int e[S::kSlots];
-#pragma unroll
-  for (int i = 0; i < S::kSlots; ++i) {
-    const bool in = g + i * G < r.k;
-    e[i] = in ? ids[g + i * G] : 0;
-    float l = key_logit(chosen[i]);
-    if (nan && in) {  // a NaN's key says -infinity
-      l = load_logit(r, token * r.E + e[i]);
-    }
-    const float x = __expf(r.sigmoid ? -l : l - mx);
-    w[i] = r.sigmoid ? __fdividef(1.0f, 1.0f + x) : x;
-    w[i] = !in || l == -INFINITY ? 0.f : w[i];  // also where the largest logit is -infinity itself
-    sum += w[i];
-  }
+  float l = key_logit(mine);
+  const float mx = __shfl_sync(0xffffffffu, l, 0);
+  if (nan && lane < r.k) l = load_logit(r, token * r.E + expert);  // a NaN's key says -infinity
+  const float e = __expf(r.sigmoid ? -l : l - mx);
+  weight = r.sigmoid ? __fdividef(1.0f, 1.0f + e) : e;
+  weight = lane >= r.k || l == -INFINITY ? 0.f : weight;  // also where the largest logit is -infinity itself
   if (r.renorm || !r.sigmoid) {
-    sum = r.renorm ? group_sum<G>(sum) : all;
+    float sum = weight;
+    if (!r.renorm) {
+      sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < S::kSlots; ++i) w[i] = sum == 0.f ? 0.f : __fdividef(w[i], sum);
+      for (int i = 0; i < L; ++i) sum += v[i] == -INFINITY ? 0.f : __expf(v[i] - mx);
+    }
+    sum = warp_sum(sum);
+    weight = sum == 0.f ? 0.f : __fdividef(weight, sum);
   }
-  if (mine < t1) {
-#pragma unroll
-    for (int i = 0; i < S::kSlots; ++i)
-      if (g + i * G < r.k) f(mine, g + i * G, e[i], w[i] * r.scale);
-  }
+  weight *= r.scale;
   __syncwarp();  // `ids` may be written again
+}
+
+// A warp's tokens t0, t0 + step, ... below t1, the next one's logits loaded (700 cycles
+// from L2) before the choice for this one: f(token, expert, weight), choice j in lane j < k.
+template <int L, bool kPacked, typename F>
+__device__ __forceinline__ void choose_all(const RouteRule& r, int64_t t0, int64_t t1, int step, int* ids, F&& f) {
+  float v[L], next[L];
+  if (t0 < t1) load_logits<L, kPacked>(r, t0, v);
+#pragma unroll 1
+  for (int64_t t = t0; t < t1; t += step) {
+    load_logits<L, kPacked>(r, min(t + step, t1 - 1), next);
+    int e;
+    float w;
+    choose_experts<L, kPacked>(r, t, v, ids, e, w);
+    f(t, e, w);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] = next[i];
+  }
+}
+template <int kMaxE, typename F>
+__device__ __forceinline__ void choose_all(const RouteRule& r, int64_t t0, int64_t t1, int step, int* ids, F&& f) {
+  for_keys_per_lane<kMaxE>(r.E, [&](auto keys) {
+    constexpr int L = decltype(keys)::value;
+    if (r.logits_f32) choose_all<L, false>(r, t0, t1, step, ids, f);
+    else choose_all<L, true>(r, t0, t1, step, ids, f);
+  });
 }
 
 // ============================================================================
@@ -263,8 +253,8 @@ struct RouteTables {
   int warp_total[kRouteThreads / 32];
 };
 
-// base[e] (0 <= e < E, counts on entry) becomes the sum of the counts before e.
-__device__ __forceinline__ void exclusive_prefix(RouteTables& s, int E) {
+// base[e] (0 <= e < E, counts on entry) becomes the sum of the counts before e, plus add[e].
+__device__ __forceinline__ void exclusive_prefix(RouteTables& s, int E, const int* add) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int carry = 0;
   for (int e0 = 0; e0 < E; e0 += kRouteThreads) {
@@ -279,30 +269,31 @@ __device__ __forceinline__ void exclusive_prefix(RouteTables& s, int E) {
     if (lane == 31) s.warp_total[warp] = inc;
     __syncthreads();
     int before = carry, total = 0;
+#pragma unroll
     for (int w = 0; w < kRouteThreads / 32; ++w) {
-      if (w < warp) before += s.warp_total[w];
+      before += w < warp ? s.warp_total[w] : 0;
       total += s.warp_total[w];
     }
-    if (e < E) s.base[e] = before + inc - c;
+    if (e < E) s.base[e] = before + inc - c + (add != nullptr ? add[e] : 0);
     carry += total;
     __syncthreads();
   }
 }
 
-// Places the choices of tokens [t0, t1), base[] holding the first free row of each expert.
+// Places the choices of tokens [t0, t1), base[] holding the first free row of each expert
+// and picked[] zeros.
 __device__ __forceinline__ void place_choices(const RouteParams& p, RouteTables& s, int64_t t0, int64_t t1) {
   const int k = p.rule.k, E = p.rule.E;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) s.picked[e] = 0ull;
-  __syncthreads();
   for (int64_t r0 = t0; r0 < t1; r0 += kRouteRun) {
     const int n = static_cast<int>(min(static_cast<int64_t>(kRouteRun), t1 - r0)) * k;
-    for (int i = threadIdx.x; i < n; i += kRouteThreads)
-      atomicOr(&s.picked[p.ids[r0 * k + i]], 1ull << (i / k));
+    const int32_t* run = p.ids + r0 * k;
+    for (int i = threadIdx.x; i < n; i += kRouteThreads) atomicOr(&s.picked[run[i]], 1ull << (i / k));
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kRouteThreads) {
-      const int e = p.ids[r0 * k + i];
+      const int e = run[i];
       p.order[s.base[e] + __popcll(s.picked[e] & ((1ull << (i / k)) - 1))] = static_cast<int32_t>(r0 * k + i);
     }
+    if (r0 + kRouteRun >= t1) break;
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
       s.base[e] += __popcll(s.picked[e]);
@@ -314,26 +305,27 @@ __device__ __forceinline__ void place_choices(const RouteParams& p, RouteTables&
 
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const __grid_constant__ RouteParams p) {
   __shared__ RouteTables s;
-  __shared__ int ids[kRouteThreads / 32 * 128];
-  const int warp = threadIdx.x >> 5;
+  __shared__ int ids[kRouteThreads];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.rule.E, k = p.rule.k;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.per_cta;
   const int64_t t1 = min(p.T, t0 + p.per_cta);
   const bool sorting = p.counts != nullptr;
   if (sorting) {
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) s.base[e] = 0;
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      s.base[e] = 0;
+      s.picked[e] = 0ull;
+    }
     __syncthreads();
   }
   pdl_wait();  // the logits may come from the kernel before
   pdl_trigger();
-  for_spread<kRouteMaxE>(E, t1 - t0 <= kRouteThreads / 32, [&](auto spread) {
-    using S = decltype(spread);
-    for (int64_t t = t0 + warp * S::kTokens; t < t1; t += kRouteThreads / 32 * S::kTokens)
-      choose_experts<S>(p.rule, t, t1, 1, ids + warp * 128, [&](int64_t token, int j, int e, float w) {
-        p.ids[token * k + j] = e;
-        p.weights[token * k + j] = w;
-        if (sorting) atomicAdd(&s.base[e], 1);
-      });
+  choose_all<kRouteMaxE>(p.rule, t0 + warp, t1, kRouteThreads / 32, ids + warp * 32, [&](int64_t t, int e, float w) {
+    if (lane < k) {
+      p.ids[t * k + lane] = e;
+      p.weights[t * k + lane] = w;
+      if (sorting) atomicAdd(&s.base[e], 1);
+    }
   });
   if (!sorting) return;
   __syncthreads();
@@ -343,7 +335,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const __gri
   }
   for (int e = threadIdx.x; e < E; e += kRouteThreads) p.counts[e] = s.base[e];
   __syncthreads();
-  exclusive_prefix(s, E);
+  exclusive_prefix(s, E, nullptr);
   place_choices(p, s, t0, t1);
 }
 
@@ -351,21 +343,31 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
   __shared__ RouteTables s;
   __shared__ int before[kRouteMaxE];  // choices of expert e in earlier CTAs
   const int E = p.rule.E, nb = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) s.base[e] = before[e] = 0;
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    s.base[e] = before[e] = 0;
+    s.picked[e] = 0ull;
+  }
   __syncthreads();
   pdl_wait();  // the counts and the choices come from the kernel before
   pdl_trigger();
-  // thread (part, e): the CTAs part, part + parts, ... of expert e; integer sums, any order
+  // thread (part, e): the CTAs part, part + parts, ... of expert e, sixteen loads in flight; integer sums, any order
   const int cols = min(E, kRouteThreads), parts = kRouteThreads / cols;
   const int part = static_cast<int>(threadIdx.x) / cols;
   if (part < parts) {
     for (int e = static_cast<int>(threadIdx.x) % cols; e < E; e += cols) {
       int total = 0, earlier = 0;
-#pragma unroll 8
-      for (int c = part; c < nb; c += parts) {
-        const int h = __ldcg(p.hist + static_cast<int64_t>(c) * E + e);
-        total += h;
-        if (c < b) earlier += h;
+      for (int c0 = part; c0 < nb; c0 += 16 * parts) {
+        int h[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int c = c0 + i * parts;
+          h[i] = c < nb ? __ldcg(p.hist + static_cast<int64_t>(c) * E + e) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          total += h[i];
+          earlier += c0 + i * parts < b ? h[i] : 0;
+        }
       }
       atomicAdd(&s.base[e], total);
       atomicAdd(&before[e], earlier);
@@ -374,10 +376,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
   __syncthreads();
   if (b == 0)
     for (int e = threadIdx.x; e < E; e += kRouteThreads) p.counts[e] = s.base[e];
-  __syncthreads();
-  exclusive_prefix(s, E);
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) s.base[e] += before[e];
-  __syncthreads();
+  exclusive_prefix(s, E, before);
   const int64_t t0 = static_cast<int64_t>(b) * p.per_cta;
   place_choices(p, s, t0, min(p.T, t0 + p.per_cta));
 }
