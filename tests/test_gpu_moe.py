@@ -140,7 +140,8 @@ def small():
 
 
 # one token to the most; experts with none, one, exactly 16, 17 and all tokens (several groups of one expert)
-@pytest.mark.parametrize("T,k", [(1, 1), (1, 8), (2, 3), (5, 2), (16, 1), (17, 8), (33, 2), (64, 4), (127, 2), (128, 8)])
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 8), (2, 3), (5, 2), (16, 1), (17, 8), (31, 3), (33, 2), (64, 4), (127, 1), (127, 2),
+                                 (128, 8)])
 @pytest.mark.parametrize("act", [mq.ACT_SILU, mq.ACT_GELU_TANH])
 def test_tokens_and_choices(small, T, k, act):
     bits, x = small.tokens(T, T)

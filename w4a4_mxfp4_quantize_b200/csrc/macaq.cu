@@ -2712,22 +2712,27 @@ static bool moe_layouts(int T, int k, int E, int H, int I, moe::Layout& up, moe:
   constexpr int kSm = 228 * 1024, kReserved = 1024;  // per SM, and per resident CTA
   constexpr int kLimit = static_cast<int>(gemm::kSmemLimit);
   const int scratch = moe::scratch_bytes(T, k, E);
+  auto fits = [&](const moe::Layout& l) { return l.bytes <= kLimit && scratch <= l.b; };
   auto pick = [&](int K, bool is_down, int limit, int least, moe::Layout& l) {
     for (int stages = moe::kMaxStages; stages >= least; --stages)
-      for (const int bufs : {is_down ? 4 : 2, is_down ? 2 : 1, 1}) {
+      for (const int bufs : {2, 1}) {
         l = moe::layout(T, k, E, K, is_down, stages, bufs);
-        if (l.bytes <= std::min(limit, kLimit) && scratch <= l.b) return true;
+        if (l.bytes <= limit && fits(l)) return true;
       }
     return false;
   };
-  down = moe::layout(T, k, E, I, true, 3, 4);
-  together = scratch <= down.b && pick(H, false, kSm - 2 * kReserved - down.bytes, 4, up);
+  down = moe::layout(T, k, E, I, true, 3, 2);
+  together = T * k <= 32 && fits(down) && pick(H, false, kSm - 2 * kReserved - down.bytes, 4, up);
   return together || (pick(H, false, kLimit, 3, up) && pick(I, true, kLimit, 3, down));
 }
 // Bytes of the groups' tables in the workspace: a bound for every E.
 static size_t moe_table_bytes(int64_t T, int64_t k) {
   const size_t tk = static_cast<size_t>(T) * k;
   return 3 * 16 + 8 * tk + 8 * (tk + tk / moe::kRows) + 32;
+}
+// Where they start, behind the codes and the scales, on 16 bytes.
+static size_t moe_table_offset(int64_t T, int64_t k, int64_t I) {
+  return (static_cast<size_t>(T) * k * (I / 2 + I / 32) + 15) / 16 * 16;
 }
 
 // Clusters of S CTAs of the down kernel that the device holds at once, with `bytes` of shared memory
@@ -2760,7 +2765,7 @@ static int moe_clusters(int dev, int S, int bytes) {
 
 size_t macaq_moe_workspace_bytes(int64_t T, int64_t k, int64_t I) {
   if (T < 1 || T > moe::kMaxTokens || k < 1 || k > moe::kMaxChoice || I < 256 || I > moe::kMaxK || I % 256 != 0) return 0;
-  return static_cast<size_t>(T) * k * (I / 2 + I / 32) + moe_table_bytes(T, k);  // codes, scales, tables
+  return moe_table_offset(T, k, I) + moe_table_bytes(T, k);
 }
 
 int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const float* D_up, const uint8_t* Wq_up,
@@ -2809,15 +2814,20 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   down.NT = down.N / kRowsTile; down.KT = down.K / kKTile;
   bool together = false;
   if (!moe_layouts(t, kk, e, up.K, down.K, up.l, down.l, together)) return MACAQ_ERR_SHAPE;
-  if (!together) up.tables = down.tables = ws + static_cast<size_t>(T) * k * (I / 2 + I / 32);
+  if (!together) up.tables = down.tables = ws + moe_table_offset(T, k, I);
   // at most T k groups (and an expert's further ones): more CTAs than that would have nothing to do
   const int groups = moe::max_groups(t, kk, e);
   const int items = groups * up.NT;
   // the largest cluster of which all fit at once (of 8, 15 do: at 2048 channels clusters of 7 take 112 SMs,
   // where 16 clusters of 8 would run one of them alone at the end and clusters of 4 take 64)
   down.S = std::min(8, groups);
-  while (down.S > 1 && moe_clusters(dev, down.S, down.l.bytes) < down.NT) --down.S;
-  if (launch_ex(moe_kernel<false>, dim3(std::min(items, sms)), dim3(moe::kUpThreads), up.l.bytes, s, true, 1, up) !=
+  const int per_sm = 228 * 1024 / (down.l.bytes + 1024);  // the occupancy query counts one CTA per SM
+  while (down.S > 1 && moe_clusters(dev, down.S, down.l.bytes) * per_sm < down.NT) --down.S;
+  // more tokens than a CTA has warps: a pair of CTAs shares the choosing (128 tokens: 90 us alone, 85 in pairs;
+  // at 16 tokens there is nothing to share, and four CTAs would leave 16 SMs out)
+  if (t > moe::kUpThreads / 32 && sms % 2 == 0) up.S = 2;
+  const int up_ctas = std::max(up.S, std::min(items, sms) / up.S * up.S);
+  if (launch_ex(moe_kernel<false>, dim3(up_ctas), dim3(moe::kUpThreads), up.l.bytes, s, true, up.S, up) !=
       cudaSuccess)
     return MACAQ_ERR_CUDA;
   return launch_ex(moe_kernel<true>, dim3(down.S * down.NT), dim3(moe::kDownThreads), down.l.bytes, s, true, down.S,

@@ -38,7 +38,7 @@ constexpr int kMaxChoice = 16;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxK = 8192;
 constexpr int kMaxStages = 8;
-constexpr int kMaxBufs = 4;
+constexpr int kMaxBufs = 2;
 constexpr int kBCodeBytes = kRows * 128;  // codes of one K tile of a group
 constexpr int kBSfBytes = 512;            // its scales: two blocks of 16 rows x 16 bytes
 constexpr int kStageBytes = kTileCodeBytes + kTileSfBytes;
@@ -61,7 +61,7 @@ __host__ __device__ inline int max_groups(int T, int k, int E) {
 }
 __host__ __device__ inline int align16i(int v) { return (v + 15) & ~15; }
 // Bytes of the tables that only choosing needs; they lie where the weight stages come later.
-__host__ __device__ inline int scratch_bytes(int T, int k, int E) { return align16i(T * k * 6) + E * 20 + kUpThreads * 4; }
+__host__ __device__ inline int scratch_bytes(int T, int k, int E) { return align16i(T * k * 8) + E * 20 + kUpThreads * 4; }
 __host__ inline Layout layout(int T, int k, int E, int K, bool down, int stages, int bufs) {
   const int KT = K / kKTile, tk = T * k, G = max_groups(T, k, E);
   Layout l;
@@ -95,7 +95,7 @@ struct MoeParams {
   int gelu;              // up: act is GELU_TANH (else SILU)
   uint8_t* tables;       // the groups' tables, copied from the up kernel's first CTA (nullptr: the down
                          // kernel chooses for itself, while the up kernel runs)
-  int S;                 // down: CTAs of a cluster
+  int S;                 // CTAs of a cluster (up: 2 where a pair shares the choosing, else 1)
   int32_t* status;
   moe::Layout l;
 };
@@ -213,13 +213,14 @@ __device__ __forceinline__ float4 ld_now(const float* p) {
 // zero is left out: it adds nothing and its expert need not be read.  Returns the number
 // of groups.  `scratch` overlaps the weight stages.
 template <int kThreads>
-__device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uint8_t* scratch, int* warp_total) {
+__device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uint8_t* scratch, int* warp_total,
+                                          int pair_rank) {
   constexpr int kWarps = kThreads / 32;
   const int k = p.rule.k, E = p.rule.E, T = p.T, tk = T * k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* sel_w = reinterpret_cast<float*>(scratch);
-  uint16_t* sel_e = reinterpret_cast<uint16_t*>(sel_w + tk);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(scratch + moe::align16i(tk * 6));  // [E][4]: tokens that chose e
+  uint32_t* sel_e = reinterpret_cast<uint32_t*>(sel_w + tk);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(scratch + moe::align16i(tk * 8));  // [E][4]: tokens that chose e
   int* off = reinterpret_cast<int*>(mask + E * 4);                                // [E]: first entry
   int* ids = off + E;                                                             // [kWarps][32]
   uint16_t* ent = reinterpret_cast<uint16_t*>(smem + p.l.ent);
@@ -228,15 +229,33 @@ __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uin
   int2* grp = reinterpret_cast<int2*>(smem + p.l.grp);
   for (int i = threadIdx.x; i < E * 4; i += kThreads) mask[i] = 0u;
   __syncthreads();
-  choose_all<moe::kMaxExperts>(p.rule, warp, T, kWarps, ids + warp * 32, [&](int64_t token, int e, float w) {
+  // a pair of CTAs takes every other round of tokens each and writes the choices to both
+  const bool paired = pair_rank >= 0;
+  const int t0 = paired ? warp + pair_rank * kWarps : warp, step = paired ? 2 * kWarps : kWarps;
+  const uint32_t other = paired ? static_cast<uint32_t>(pair_rank ^ 1) : 0u;
+  if (paired) cluster_wait_acquire();  // the other CTA runs
+  choose_all<moe::kMaxExperts>(p.rule, t0, T, step, ids + warp * 32, [&](int64_t token, int e, float w) {
     if (lane < k) {
-      const int t = static_cast<int>(token);
-      const bool used = w != 0.f;
-      sel_w[t * k + lane] = w;
-      sel_e[t * k + lane] = used ? static_cast<uint16_t>(e) : 0xFFFFu;
-      if (used) atomicOr(&mask[e * 4 + (t >> 5)], 1u << (t & 31));
+      const int i = static_cast<int>(token) * k + lane;
+      const uint32_t ee = w != 0.f ? static_cast<uint32_t>(e) : 0xFFFFu;
+      sel_w[i] = w;
+      sel_e[i] = ee;
+      if (paired) {
+        st_dsmem_b32(mapa_shared(smem_u32(sel_w + i), other), __float_as_uint(w));
+        st_dsmem_b32(mapa_shared(smem_u32(sel_e + i), other), ee);
+      } else if (ee != 0xFFFFu) {
+        atomicOr(&mask[ee * 4 + (token >> 5)], 1u << (token & 31));
+      }
     }
   });
+  if (paired) {
+    cluster_sync_all();
+    for (int i = threadIdx.x; i < tk; i += kThreads) {
+      const uint32_t e = sel_e[i];
+      const int t = i / k;
+      if (e != 0xFFFFu) atomicOr(&mask[e * 4 + (t >> 5)], 1u << (t & 31));
+    }
+  }
   __syncthreads();
   // entries and groups before each expert, one expert per thread
   int ent_base = 0, grp_base = 0;
@@ -273,7 +292,7 @@ __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uin
     __syncthreads();
   }
   for (int i = threadIdx.x; i < tk; i += kThreads) {
-    const int e = sel_e[i];
+    const int e = static_cast<int>(sel_e[i]);
     if (e != 0xFFFF) {
       const int t = i / k;
       int r = off[e] + __popc(mask[e * 4 + (t >> 5)] & ((1u << (t & 31)) - 1));
@@ -335,6 +354,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
     fence_mbar_init();
   }
   if constexpr (!kDown) {
+    if (p.S == 2) cluster_arrive_release();
     pdl_wait();  // x and the logits may come from the kernel before
     // The down kernel may start: what it reads before its own wait is complete.  Warp 1 says so, after
     // its tensor memory is allocated: a CTA of the down kernel may take the rest of it and wait for us.
@@ -352,7 +372,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
     G = *reinterpret_cast<const int*>(src + table_words);
     __syncthreads();
   } else {
-    G = moe_groups<kThreads>(p, smem, smem, warp_total);
+    G = moe_groups<kThreads>(p, smem, smem, warp_total, !kDown && p.S == 2 ? static_cast<int>(cluster_ctarank()) : -1);
     if (!kDown && p.tables != nullptr && blockIdx.x == 0) {
       uint4* dst = reinterpret_cast<uint4*>(p.tables);
       for (int i = threadIdx.x; i < table_words; i += kThreads) dst[i] = reinterpret_cast<const uint4*>(smem + p.l.ent)[i];
@@ -507,51 +527,43 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
   } else if (warp == 3) {
     if constexpr (kDown) {
       // ---- the groups' activations into the tensor core's layout: codes in 16-byte pieces, scales in
-      // words of four blocks, `lag` groups in flight behind the one being issued ----
+      // words of four blocks ----
       pdl_wait();  // they come from the up kernel
       pdl_trigger();
-      const int n = g1 - g0, lag = bufs > 2 ? 2 : 0;
       const int code_row = p.K / 2, sf_row = p.K / 32;
-      int buf = 0, done = 0;  // buffers of the group being issued and of the next to have landed
+      int buf = 0;
       uint32_t turn = 1;
-      for (int i = 0; i < n + lag; ++i) {
-        if (i < n) {
-          if (!mbar_wait_warp(&bempty[buf], turn, abort_flag, kWaitTimeoutNs)) break;
-          const int2 gr = grp[g0 + i];
-          const int first = gr.x, rows = gr.y >> 16;
-          uint8_t* bq = smem + p.l.b + buf * KT * kBCodeBytes;
-          uint8_t* bs = smem + p.l.bsf + buf * KT * kBSfBytes;
-          // lane: piece c of row j, four rows at a time (lanes past the last row repeat it)
-          const int c = lane & 7;
-          for (int j0 = 0; j0 < rows; j0 += 4) {
-            const int j = min(j0 + (lane >> 3), rows - 1);
-            const int e = ent[first + j];
-            const uint8_t* src = p.codes + static_cast<int64_t>(e) * code_row + c * 16;
-            uint8_t* dst = bq + code_chunk_offset(j, c);
+      for (int g = g0; g < g1; ++g) {
+        if (!mbar_wait_warp(&bempty[buf], turn, abort_flag, kWaitTimeoutNs)) break;
+        const int2 gr = grp[g];
+        const int first = gr.x, rows = gr.y >> 16;
+        uint8_t* bq = smem + p.l.b + buf * KT * kBCodeBytes;
+        uint8_t* bs = smem + p.l.bsf + buf * KT * kBSfBytes;
+        // lane: piece c of row j, four rows at a time (lanes past the last row repeat it)
+        const int c = lane & 7;
+        for (int j0 = 0; j0 < rows; j0 += 4) {
+          const int j = min(j0 + (lane >> 3), rows - 1);
+          const int e = ent[first + j];
+          const uint8_t* src = p.codes + static_cast<int64_t>(e) * code_row + c * 16;
+          uint8_t* dst = bq + code_chunk_offset(j, c);
 #pragma unroll 4
-            for (int kt = 0; kt < KT; ++kt) cp_async16(dst + kt * kBCodeBytes, src + kt * 128);
-            const uint8_t* sf = p.scales + static_cast<int64_t>(e) * sf_row;
-            for (int w0 = 0; w0 < 2 * KT; w0 += 8) {
-              const int w = min(w0 + c, 2 * KT - 1);
-              cp_async4(bs + (w >> 1) * kBSfBytes + (w & 1) * 256 + j * 16, sf + w * 4);
-            }
-          }
-          if (++buf == bufs) {
-            buf = 0;
-            turn ^= 1;
+          for (int kt = 0; kt < KT; ++kt) cp_async16(dst + kt * kBCodeBytes, src + kt * 128);
+          const uint8_t* sf = p.scales + static_cast<int64_t>(e) * sf_row;
+          for (int w0 = 0; w0 < 2 * KT; w0 += 8) {
+            const int w = min(w0 + c, 2 * KT - 1);
+            cp_async4(bs + (w >> 1) * kBSfBytes + (w & 1) * 256 + j * 16, sf + w * 4);
           }
         }
         cp_async_commit();
-        if (i >= lag) {
-          if (lag == 2) cp_async_wait<2>();
-          else cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bfull[done]);
-          if (++done == bufs) done = 0;
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bfull[buf]);
+        if (++buf == bufs) {
+          buf = 0;
+          turn ^= 1;
         }
       }
-      cp_async_wait<0>();  // no copy may still be writing this CTA's shared memory at exit
     }
   } else if (warp < 8) {
     // ---- epilogue: 16 accumulator columns (tokens) of this thread's weight row ----
