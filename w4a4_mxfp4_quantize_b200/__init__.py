@@ -17,6 +17,7 @@ import contextlib
 import ctypes
 import os
 import subprocess
+import sysconfig
 import threading
 
 import torch
@@ -24,6 +25,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 _LIB_PATH = os.path.join(_HERE, "libmacaq.so")
+_BINDING_PATH = os.path.join(_HERE, "_binding.so")
 _SRC = os.path.join(_HERE, "csrc", "macaq.cu")
 _INCLUDE = os.path.join(_ROOT, "include")
 
@@ -51,21 +53,36 @@ class MacaqError(RuntimeError):
         self.status = status
 
 
-def _sources():
+def _sources(suffixes: tuple[str, ...] = (".cu", ".cuh", ".cpp")):
     d = os.path.join(_HERE, "csrc")
-    return [os.path.join(d, f) for f in sorted(os.listdir(d))] + [os.path.join(_INCLUDE, "macaq.h")]
+    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith(suffixes)] + [os.path.join(_INCLUDE, "macaq.h")]
+
+
+def _older(path: str, sources) -> bool:
+    return not os.path.exists(path) or os.path.getmtime(path) < max(os.path.getmtime(f) for f in sources)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libmacaq.so for sm_100a in-tree (nvcc cross-compiles without a GPU)."""
-    newest = max(os.path.getmtime(f) for f in _sources())
-    if force or not os.path.exists(_LIB_PATH) or os.path.getmtime(_LIB_PATH) < newest:
+    """Compile libmacaq.so for sm_100a in-tree (nvcc cross-compiles without a GPU), and the
+    module with the short way to the calls around the linear (_binding.so, g++)."""
+    if force or _older(_LIB_PATH, _sources((".cu", ".cuh"))):
         tmp = _LIB_PATH + f".tmp{os.getpid()}"
         cmd = ["nvcc", *NVCC_FLAGS, "-I" + _INCLUDE, "-o", tmp, _SRC]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.check_call(cmd)
         os.replace(tmp, _LIB_PATH)
+    if force or _older(_BINDING_PATH, _sources((".cpp",))):
+        from torch.utils import cpp_extension
+
+        tmp = _BINDING_PATH + f".tmp{os.getpid()}"
+        include = [_INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
+        subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp,
+                               os.path.join(_HERE, "csrc", "binding.cpp"), *("-I" + d for d in include),
+                               *("-L" + d for d in cpp_extension.library_paths("cuda")), "-L" + _HERE,
+                               "-l:" + os.path.basename(_LIB_PATH), "-Wl,-rpath,$ORIGIN", "-ltorch_python", "-ltorch",
+                               "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
+        os.replace(tmp, _BINDING_PATH)
     return _LIB_PATH
 
 
@@ -138,8 +155,22 @@ def lib() -> ctypes.CDLL:
                     f = getattr(L, name)
                     f.restype = res
                     f.argtypes = args
+                _load_binding()
                 _lib = L
     return _lib
+
+
+# The compiled short way (csrc/binding.cpp): None where it was not built, and the calls
+# then go through ctypes alone.
+_fast = None
+
+
+def _load_binding():
+    global _fast
+    if os.path.exists(_BINDING_PATH):
+        from . import _binding
+
+        _fast = _binding
 
 
 def exported_symbols() -> list[str]:
@@ -663,24 +694,18 @@ def _at(t):
 def _place(stream, *ts):
     """Where a call runs: every tensor contiguous on the first one's device (its index is
     returned), and the context that makes that device and the stream current, None where
-    they are.  These calls take a few microseconds on the GPU: their checks are kept to
-    what costs a tenth of one."""
+    they are."""
     dev = ts[0].get_device()
     for t in ts:
-        if t is not None and (dev < 0 or t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError("expected contiguous CUDA tensors on one device")
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            dev = -1
+    if dev < 0:
+        raise ValueError("expected contiguous CUDA tensors on one device")
     if stream is not None:
         if stream.device.index != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
         return dev, torch.cuda.stream(stream)  # makes its device current too
     return dev, None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _within(context, f, *args):
-    if context is None:
-        return f(*args)
-    with context:
-        return f(*args)
 
 
 def _scratch(nbytes: int, dev: int, given: torch.Tensor | None):
@@ -713,6 +738,12 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Ten
     (h' is h); w_post, w_pre fp32 [C] (None: no norm there; without w_pre n is None); gate
     bf16 or fp32, [C] for one gate of all rows or [G, C] where row m takes gate row
     m // rows_per_gate (default 1: one per row)."""
+    if _fast is not None and stream is None and out_h is None and out_n is None:
+        r = _fast.block_norm(h, y, w_post, gate, rows_per_gate, w_pre, scale, eps, weight_offset)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            raise MacaqError(r, "macaq_block_norm")
     h_type = _element_type(h, "h")
     shape = h.shape
     if len(shape) != 2:
@@ -746,8 +777,9 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Ten
             want = (-(-M // per), C)
         _shape(gate, "gate", gate.dtype, want)
     dev, context = _place(stream, h, y, w_post, gate, w_pre, out_h, out_n)
-    return _within(context, _block_norm, h, h_type, y, w_post, gate, gate_type, per, w_pre, scale, eps, weight_offset,
-                   out_h, out_n, M, C, dev)
+    with context or contextlib.nullcontext():
+        return _block_norm(h, h_type, y, w_post, gate, gate_type, per, w_pre, scale, eps, weight_offset, out_h, out_n,
+                           M, C, dev)
 
 
 def _block_norm(h, h_type, y, w_post, gate, gate_type, per, w_pre, scale, eps, weight_offset, out_h, out_n, M, C, dev):
@@ -755,10 +787,9 @@ def _block_norm(h, h_type, y, w_post, gate, gate_type, per, w_pre, scale, eps, w
         out_h = torch.empty_like(h)
     if w_pre is not None and out_n is None:
         out_n = torch.empty_like(h, dtype=torch.bfloat16)
-    st = lib().macaq_block_norm(h.data_ptr(), h_type, _at(y), _at(w_post), _at(gate), gate_type, per, _at(w_pre),
-                                scale, eps, weight_offset, _at(out_h), _at(out_n), M, C, _raw_stream(dev))
-    if st:
-        raise MacaqError(st, "macaq_block_norm")
+    _check(lib().macaq_block_norm(_at(h), h_type, _at(y), _at(w_post), _at(gate), gate_type, per, _at(w_pre), scale,
+                                  eps, weight_offset, _at(out_h), _at(out_n), M, C, _raw_stream(dev)),
+           "macaq_block_norm")
     return (h if y is None else out_h), out_n
 
 
@@ -768,6 +799,12 @@ def moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renorm: 
     counts int64 [E], order int32 [T k]); row r of the rows sorted by expert belongs to
     token order[r] // k, and counts is grouped_mm's group_list of type 1 for them.
     counts and order are None without sort."""
+    if _fast is not None and sort and stream is None and ws is None:
+        r = _fast.moe_route(logits, k, score, renorm, scale)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            raise MacaqError(r, "macaq_moe_route")
     logits_type = _element_type(logits, "logits")
     shape = logits.shape
     if len(shape) != 2:
@@ -776,7 +813,8 @@ def moe_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, renorm: 
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be between 1 and min(E, 32) = {min(E, 32)}, got {k}")
     dev, context = _place(stream, logits, ws)
-    return _within(context, _moe_route, logits, logits_type, T, E, k, score, renorm, scale, sort, ws, dev)
+    with context or contextlib.nullcontext():
+        return _moe_route(logits, logits_type, T, E, k, score, renorm, scale, sort, ws, dev)
 
 
 def _moe_route(logits, logits_type, T, E, k, score, renorm, scale, sort, ws, dev):
@@ -789,11 +827,9 @@ def _moe_route(logits, logits_type, T, E, k, score, renorm, scale, sort, ws, dev
         counts = _empty((E,), (1,), dtype=torch.int64, device=device)
         order = _empty((T * k,), (1,), dtype=torch.int32, device=device)
         ws = _scratch(L.macaq_route_workspace_bytes(T, E), dev, ws)
-    st = L.macaq_moe_route(logits.data_ptr(), logits_type, T, E, k, score, 1 if renorm else 0, scale, ids.data_ptr(),
-                           weights.data_ptr(), _at(counts), _at(order) if T else None, _at(ws), _nbytes(ws),
-                           _raw_stream(dev))
-    if st:
-        raise MacaqError(st, "macaq_moe_route")
+    _check(L.macaq_moe_route(_at(logits), logits_type, T, E, k, score, 1 if renorm else 0, scale, _at(ids),
+                             _at(weights), _at(counts), _at(order) if T else None, _at(ws), _nbytes(ws),
+                             _raw_stream(dev)), "macaq_moe_route")
     return ids, weights, counts, order
 
 
@@ -810,7 +846,8 @@ def prepare_gate_up(W: torch.Tensor, D: torch.Tensor, stream=None) -> tuple[torc
         raise ValueError(f"W holds as many gate rows as up rows, got {N} rows")
     _shape(D, "D", torch.float32, (E, K))
     dev, context = _place(stream, W, D)
-    return _within(context, _prepare_gate_up, W, D, E, N, K, dev)
+    with context or contextlib.nullcontext():
+        return _prepare_gate_up(W, D, E, N, K, dev)
 
 
 def _prepare_gate_up(W, D, E, N, K, dev):
@@ -837,6 +874,13 @@ def moe_mm(x: torch.Tensor, logits: torch.Tensor, D_up: torch.Tensor, Wq_up: tor
     and the router's logits bf16 or fp32 [T, E], the experts chosen and weighted as by
     moe_route.  D_up fp32 [E, H] with the images of prepare_gate_up, D_down fp32 [E, inner]
     with those of prepare_weights ([E, H, inner])."""
+    if _fast is not None and stream is None and out is None and status is None and ws is None:
+        r = _fast.moe_mm(x, logits, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, inner, k, score, renorm, scale,
+                         act_type)
+        if r.__class__ is int:
+            raise MacaqError(r, "macaq_moe_mm")
+        if r is not None:
+            return r
     _arg(x, "x", torch.bfloat16, ndim=2)
     logits_type = _element_type(logits, "logits")
     T, H = x.shape
@@ -854,8 +898,9 @@ def moe_mm(x: torch.Tensor, logits: torch.Tensor, D_up: torch.Tensor, Wq_up: tor
     _arg(Wq_down, "Wq_down", torch.uint8, min_numel=L.macaq_weight_code_bytes(E, H, inner))
     _arg(Ws_down, "Ws_down", torch.uint8, min_numel=L.macaq_weight_scale_bytes(E, H, inner))
     dev, context = _place(stream, x, logits, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, out, status, ws)
-    return _within(context, _moe_mm, x, logits, logits_type, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, T, E, k, H,
-                   inner, score, renorm, scale, act_type, out, ws, status, dev)
+    with context or contextlib.nullcontext():
+        return _moe_mm(x, logits, logits_type, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, T, E, k, H, inner, score,
+                       renorm, scale, act_type, out, ws, status, dev)
 
 
 def _moe_mm(x, logits, logits_type, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down, T, E, k, H, inner, score, renorm,
@@ -863,10 +908,7 @@ def _moe_mm(x, logits, logits_type, D_up, Wq_up, Ws_up, D_down, Wq_down, Ws_down
     L = lib()
     y = torch.empty_like(x) if out is None else out
     ws = _scratch(L.macaq_moe_workspace_bytes(T, k, inner), dev, ws)
-    st = L.macaq_moe_mm(x.data_ptr(), logits.data_ptr(), logits_type, D_up.data_ptr(), Wq_up.data_ptr(),
-                        Ws_up.data_ptr(), D_down.data_ptr(), Wq_down.data_ptr(), Ws_down.data_ptr(), T, E, k, H, inner,
-                        score, 1 if renorm else 0, scale, act_type, y.data_ptr(), _at(ws), _nbytes(ws), _at(status),
-                        _raw_stream(dev))
-    if st:
-        raise MacaqError(st, "macaq_moe_mm")
+    _check(L.macaq_moe_mm(_at(x), _at(logits), logits_type, _at(D_up), _at(Wq_up), _at(Ws_up), _at(D_down),
+                          _at(Wq_down), _at(Ws_down), T, E, k, H, inner, score, 1 if renorm else 0, scale, act_type,
+                          _at(y), _at(ws), _nbytes(ws), _at(status), _raw_stream(dev)), "macaq_moe_mm")
     return y
