@@ -465,8 +465,8 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
         if (!mbar_wait_warp(&acce[ab], ((w.i >> 1) & 1) ^ 1, abort_flag, kWaitTimeoutNs)) break;
         tc_fence_after();
         for (int kt = 0; kt < KT; ++kt) {
-          if (!mbar_wait_warp(&full[stage], phase, abort_flag, kWaitTimeoutNs) ||
-              !mbar_wait_warp(&sfull[stage], phase, abort_flag, kWaitTimeoutNs)) {
+          // the scales are copied once the stage is complete: their arrival stands for both
+          if (!mbar_wait_warp(&sfull[stage], phase, abort_flag, kWaitTimeoutNs)) {
             ok = false;
             break;
           }
