@@ -152,6 +152,8 @@ def test_norm_refused_by_name(L):
         assert f(**{name: at(9, 8)}) == -2, name
     size = 64 * 1024 * 2
     assert f(ho=at(1, 16)) == -5            # in place means the same rows
+    assert f(ho=at(1)) == -8                # (accepted: the missing device is the next refusal)
+    assert f(y=at(1), ho=at(1)) == -5       # in place, and the branch in the same memory
     assert f(ho=at(2)) == f(no=at(1)) == f(no=at(2)) == f(no=at(6, size - 16)) == f(ho=at(3)) == f(no=at(4)) == -5
     assert f(ho=at(4, size - 16)) == -5     # the gate of the last row
     assert f(g=at(4), per=64, ho=at(4, 2048)) != -5  # one gate row: behind it is free

@@ -192,6 +192,7 @@ def test_masked_tokens_give_zeros(small):
     logits[:] = -INF
     y = mq.moe_mm(x, logits, *small.args, inner=small.I, k=k)
     assert (y == 0).all()
+    assert mq.moe_mm(x[:0], logits[:0], *small.args, inner=small.I, k=k).shape == (0, small.H)
 
 
 def test_non_finite_tokens_stay_in_their_rows(small):

@@ -2613,7 +2613,8 @@ int macaq_block_norm(const void* h, int h_type, const uint16_t* y, const float* 
   if (!aligned16(h_out) || !aligned16(n_out)) return MACAQ_ERR_ALIGN;
   for (const auto& i : in) {
     if (i.p == nullptr) continue;
-    if (h_out != nullptr && !(i.p == h && h_out == h) && overlaps(h_out, hb, i.p, i.n)) return MACAQ_ERR_ALIAS;
+    const bool in_place = &i == &in[0] && h_out == h;
+    if (h_out != nullptr && !in_place && overlaps(h_out, hb, i.p, i.n)) return MACAQ_ERR_ALIAS;
     if (n_out != nullptr && overlaps(n_out, yb, i.p, i.n)) return MACAQ_ERR_ALIAS;
   }
   if (h_out != nullptr && n_out != nullptr && overlaps(h_out, hb, n_out, yb)) return MACAQ_ERR_ALIAS;

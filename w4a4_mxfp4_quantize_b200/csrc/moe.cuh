@@ -458,9 +458,13 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
       const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(smem)), b0 = sdesc_kmajor_sw128(smem_u32(smem + p.l.b));
       int stage = 0;
       uint32_t phase = 0;
+      uint64_t ad = a0;  // the stage's weights and scales, stepped along with it
+      uint32_t sf = tmem + kSfCol;
       bool ok = true;
       for (Walk w = walk(); w.i < n_items && ok; next_item(w)) {
         const int ab = w.i & 1;
+        uint64_t bd = b0 + (static_cast<uint32_t>(w.buf * KT * kBCodeBytes) >> 4);
+        const uint32_t acc = tmem + ab * kRows;
         if (w.fresh && !mbar_wait_warp(&bfull[w.buf], w.turn, abort_flag, kWaitTimeoutNs)) break;
         if (!mbar_wait_warp(&acce[ab], ((w.i >> 1) & 1) ^ 1, abort_flag, kWaitTimeoutNs)) break;
         tc_fence_after();
@@ -471,17 +475,19 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
             break;
           }
           tc_fence_after();
-          const uint32_t sf = tmem + kSfCol + 16 * stage;
           if (elect_one()) {
-            mma_stage(a0 + (static_cast<uint32_t>(stage * kTileCodeBytes) >> 4),
-                      b0 + (static_cast<uint32_t>((w.buf * KT + kt) * kBCodeBytes) >> 4), sf, sf + 8, tmem + ab * kRows,
-                      idesc_lo, idesc_hi, kt == 0);
+            mma_stage(ad, bd, sf, sf + 8, acc, idesc_lo, idesc_hi, kt == 0);
             tc_commit(&empty[stage]);
           }
           __syncwarp();
+          ad += kTileCodeBytes >> 4;
+          bd += kBCodeBytes >> 4;
+          sf += 16;
           if (++stage == stages) {
             stage = 0;
             phase ^= 1;
+            ad = a0;
+            sf = tmem + kSfCol;
           }
         }
         if (!ok) break;
@@ -498,17 +504,17 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
       const uint64_t sfa0 = sdesc_sf_block(smem_u32(smem + p.l.sf)), sfb0 = sdesc_sf_block(smem_u32(smem + p.l.bsf));
       int stage = 0;
       uint32_t phase = 0;
+      uint64_t sa = sfa0;
+      uint32_t sf = tmem + kSfCol;
       bool ok = true;
       for (Walk w = walk(); w.i < n_items && ok; next_item(w)) {
+        uint64_t sb = sfb0 + (static_cast<uint32_t>(w.buf * KT * kBSfBytes) >> 4);
         if (w.fresh && !mbar_wait_warp(&bfull[w.buf], w.turn, abort_flag, kWaitTimeoutNs)) break;
         for (int kt = 0; kt < KT; ++kt) {
           if (!mbar_wait_warp(&full[stage], phase, abort_flag, kWaitTimeoutNs)) {
             ok = false;
             break;
           }
-          const uint32_t sf = tmem + kSfCol + 16 * stage;
-          const uint64_t sa = sfa0 + (static_cast<uint32_t>(stage * kTileSfBytes) >> 4);
-          const uint64_t sb = sfb0 + (static_cast<uint32_t>((w.buf * KT + kt) * kBSfBytes) >> 4);
           if (elect_one()) {
             tc_cp_32x128b_warpx4(sf, sa);
             tc_cp_32x128b_warpx4(sf + 4, sa + (512 >> 4));
@@ -517,9 +523,14 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
             tc_commit(&sfull[stage]);
           }
           __syncwarp();
+          sa += kTileSfBytes >> 4;
+          sb += kBSfBytes >> 4;
+          sf += 16;
           if (++stage == stages) {
             stage = 0;
             phase ^= 1;
+            sa = sfa0;
+            sf = tmem + kSfCol;
           }
         }
       }
