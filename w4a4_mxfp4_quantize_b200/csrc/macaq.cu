@@ -2735,16 +2735,16 @@ static size_t moe_table_offset(int64_t T, int64_t k, int64_t I) {
   return (static_cast<size_t>(T) * k * (I / 2 + I / 32) + 15) / 16 * 16;
 }
 
-// Clusters of S CTAs of the down kernel that the device holds at once, with `bytes` of shared memory
-// each; asked once per device, S and whole number of KiB.
-static int moe_clusters(int dev, int S, int bytes) {
-  static int16_t cache[kMaxDevices][8][228] = {};
+// Clusters of S CTAs of a kernel that the device holds at once, with `bytes` of shared memory each;
+// asked once per device, kernel, S and whole number of KiB.
+static int moe_clusters(int dev, bool down, int S, int bytes) {
+  static int16_t cache[kMaxDevices][2][8][228] = {};
   const int kib = (bytes + 1023) / 1024;
-  int16_t& v = cache[dev][S - 1][kib - 1];
+  int16_t& v = cache[dev][down ? 1 : 0][S - 1][kib - 1];
   if (v == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S);
-    cfg.blockDim = dim3(moe::kDownThreads);
+    cfg.blockDim = dim3(down ? moe::kDownThreads : moe::kUpThreads);
     cfg.dynamicSmemBytes = std::min<size_t>(static_cast<size_t>(kib) * 1024, gemm::kSmemLimit);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -2754,7 +2754,7 @@ static int moe_clusters(int dev, int S, int bytes) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, moe_kernel<true>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, down ? moe_kernel<true> : moe_kernel<false>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 1;
     }
@@ -2822,11 +2822,12 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   // where 16 clusters of 8 would run one of them alone at the end and clusters of 4 take 64)
   down.S = std::min(8, groups);
   const int per_sm = 228 * 1024 / (down.l.bytes + 1024);  // the occupancy query counts one CTA per SM
-  while (down.S > 1 && moe_clusters(dev, down.S, down.l.bytes) * per_sm < down.NT) --down.S;
-  // more tokens than a CTA has warps: a pair of CTAs shares the choosing (128 tokens: 90 us alone, 85 in pairs;
-  // at 16 tokens there is nothing to share, and four CTAs would leave 16 SMs out)
-  if (t > moe::kUpThreads / 32 && sms % 2 == 0) up.S = 2;
-  const int up_ctas = std::max(up.S, std::min(items, sms) / up.S * up.S);
+  while (down.S > 1 && moe_clusters(dev, true, down.S, down.l.bytes) * per_sm < down.NT) --down.S;
+  // More tokens than a CTA has warps: a cluster shares the choosing.  Of 128 experts: 128 tokens 90 us alone, 84
+  // in pairs, 81 in fours (which leave 16 SMs out); 64 tokens 75, 71 and 69; 32 tokens 62, 60 and 60.
+  up.S = t > moe::kUpThreads / 16 ? 4 : t > moe::kUpThreads / 32 ? 2 : 1;
+  const int up_max = up.S == 1 ? sms : up.S * std::max(1, moe_clusters(dev, false, up.S, up.l.bytes));
+  const int up_ctas = std::max(up.S, std::min(items, up_max) / up.S * up.S);
   if (launch_ex(moe_kernel<false>, dim3(up_ctas), dim3(moe::kUpThreads), up.l.bytes, s, true, up.S, up) !=
       cudaSuccess)
     return MACAQ_ERR_CUDA;

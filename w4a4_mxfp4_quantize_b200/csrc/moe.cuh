@@ -95,7 +95,7 @@ struct MoeParams {
   int gelu;              // up: act is GELU_TANH (else SILU)
   uint8_t* tables;       // the groups' tables, copied from the up kernel's first CTA (nullptr: the down
                          // kernel chooses for itself, while the up kernel runs)
-  int S;                 // CTAs of a cluster (up: 2 where a pair shares the choosing, else 1)
+  int S;                 // CTAs of a cluster (up: those that share the choosing)
   int32_t* status;
   moe::Layout l;
 };
@@ -214,7 +214,7 @@ __device__ __forceinline__ float4 ld_now(const float* p) {
 // of groups.  `scratch` overlaps the weight stages.
 template <int kThreads>
 __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uint8_t* scratch, int* warp_total,
-                                          int pair_rank) {
+                                          int share, int shares) {
   constexpr int kWarps = kThreads / 32;
   const int k = p.rule.k, E = p.rule.E, T = p.T, tk = T * k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -229,26 +229,26 @@ __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uin
   int2* grp = reinterpret_cast<int2*>(smem + p.l.grp);
   for (int i = threadIdx.x; i < E * 4; i += kThreads) mask[i] = 0u;
   __syncthreads();
-  // a pair of CTAs takes every other round of tokens each and writes the choices to both
-  const bool paired = pair_rank >= 0;
-  const int t0 = paired ? warp + pair_rank * kWarps : warp, step = paired ? 2 * kWarps : kWarps;
-  const uint32_t other = paired ? static_cast<uint32_t>(pair_rank ^ 1) : 0u;
-  if (paired) cluster_wait_acquire();  // the other CTA runs
-  choose_all<moe::kMaxExperts>(p.rule, t0, T, step, ids + warp * 32, [&](int64_t token, int e, float w) {
+  // the CTAs of a cluster share the tokens, and each writes its choices to all of them
+  if (shares > 1) cluster_wait_acquire();  // the others run
+  choose_all<moe::kMaxExperts>(p.rule, warp + share * kWarps, T, shares * kWarps, ids + warp * 32, [&](int64_t token, int e, float w) {
     if (lane < k) {
       const int i = static_cast<int>(token) * k + lane;
       const uint32_t ee = w != 0.f ? static_cast<uint32_t>(e) : 0xFFFFu;
       sel_w[i] = w;
       sel_e[i] = ee;
-      if (paired) {
-        st_dsmem_b32(mapa_shared(smem_u32(sel_w + i), other), __float_as_uint(w));
-        st_dsmem_b32(mapa_shared(smem_u32(sel_e + i), other), ee);
+      if (shares > 1) {
+        for (int o = 1; o < shares; ++o) {
+          const uint32_t other = static_cast<uint32_t>(share + o < shares ? share + o : share + o - shares);
+          st_dsmem_b32(mapa_shared(smem_u32(sel_w + i), other), __float_as_uint(w));
+          st_dsmem_b32(mapa_shared(smem_u32(sel_e + i), other), ee);
+        }
       } else if (ee != 0xFFFFu) {
         atomicOr(&mask[ee * 4 + (token >> 5)], 1u << (token & 31));
       }
     }
   });
-  if (paired) {
+  if (shares > 1) {
     cluster_sync_all();
     for (int i = threadIdx.x; i < tk; i += kThreads) {
       const uint32_t e = sel_e[i];
@@ -354,7 +354,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
     fence_mbar_init();
   }
   if constexpr (!kDown) {
-    if (p.S == 2) cluster_arrive_release();
+    if (p.S > 1) cluster_arrive_release();
     pdl_wait();  // x and the logits may come from the kernel before
     // The down kernel may start: what it reads before its own wait is complete.  Warp 1 says so, after
     // its tensor memory is allocated: a CTA of the down kernel may take the rest of it and wait for us.
@@ -372,7 +372,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
     G = *reinterpret_cast<const int*>(src + table_words);
     __syncthreads();
   } else {
-    G = moe_groups<kThreads>(p, smem, smem, warp_total, !kDown && p.S == 2 ? static_cast<int>(cluster_ctarank()) : -1);
+    G = moe_groups<kThreads>(p, smem, smem, warp_total, kDown ? 0 : static_cast<int>(cluster_ctarank()), kDown ? 1 : p.S);
     if (!kDown && p.tables != nullptr && blockIdx.x == 0) {
       uint4* dst = reinterpret_cast<uint4*>(p.tables);
       for (int i = threadIdx.x; i < table_words; i += kThreads) dst[i] = reinterpret_cast<const uint4*>(smem + p.l.ent)[i];
