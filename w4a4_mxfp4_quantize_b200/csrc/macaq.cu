@@ -2712,17 +2712,21 @@ static bool moe_layouts(int T, int k, int E, int H, int I, moe::Layout& up, moe:
   constexpr int kSm = 228 * 1024, kReserved = 1024;  // per SM, and per resident CTA
   constexpr int kLimit = static_cast<int>(gemm::kSmemLimit);
   const int scratch = moe::scratch_bytes(T, k, E);
-  auto fits = [&](const moe::Layout& l) { return l.bytes <= kLimit && scratch <= l.b; };
+  auto fits = [&](const moe::Layout& l, bool is_down) {
+    // at the end of the down kernel the other CTAs' sums, T rows in all, lie where stages and buffers were
+    const int rows = is_down && T > moe::kFewTokens ? (T + 7) * kRowsTile * 4 : 0;
+    return l.bytes <= kLimit && scratch <= l.b && rows <= l.bar;
+  };
   auto pick = [&](int K, bool is_down, int limit, int least, moe::Layout& l) {
     for (int stages = moe::kMaxStages; stages >= least; --stages)
       for (const int bufs : {2, 1}) {
         l = moe::layout(T, k, E, K, is_down, stages, bufs);
-        if (l.bytes <= limit && fits(l)) return true;
+        if (l.bytes <= limit && fits(l, is_down)) return true;
       }
     return false;
   };
   down = moe::layout(T, k, E, I, true, 3, 2);
-  together = T * k <= 32 && fits(down) && pick(H, false, kSm - 2 * kReserved - down.bytes, 4, up);
+  together = T * k <= 32 && fits(down, true) && pick(H, false, kSm - 2 * kReserved - down.bytes, 4, up);
   return together || (pick(H, false, kLimit, 3, up) && pick(I, true, kLimit, 3, down));
 }
 // Bytes of the groups' tables in the workspace: a bound for every E.
