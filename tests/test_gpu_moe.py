@@ -275,6 +275,21 @@ def test_repeated_calls_streams_graphs_and_devices(small):
     assert torch.equal(y, want[0])
 
 
+def test_many_small_calls_at_once():
+    # three CTAs of the second kernel share an SM here, of one call and of several: clusters of CTAs that wait for
+    # one another, each with tensor memory of its own
+    layer, T, k = Layer(8, 8192, 256, seed=21), 8, 2
+    bits, x = layer.tokens(T, 22)
+    logits = layer.logits(T, 23)
+    check(layer, bits, x, logits, k)
+    want = mq.moe_mm(x, logits, *layer.args, inner=256, k=k).clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [mq.moe_mm(x, logits, *layer.args, inner=256, k=k, stream=s) for _ in range(25) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
+
+
 def test_a_block_as_it_is_used(small):
     # norm -> router logits -> layer -> norm with the residual, twice, captured and replayed
     T, k, H = 12, 2, small.H

@@ -43,14 +43,18 @@ constexpr int kMaxBufs = 2;
 constexpr int kBCodeBytes = kRows * 128;  // codes of one K tile of a group
 constexpr int kBSfBytes = 512;            // its scales: two blocks of 16 rows x 16 bytes
 constexpr int kStageBytes = kTileCodeBytes + kTileSfBytes;
-constexpr int kTmemCols = 256;            // two accumulators of 16 columns, then 16 scale columns a stage
-constexpr int kSfCol = 32;
+constexpr int kSfCol = 32;                // tensor memory: two accumulators of 16 columns, then 16 scale columns a stage
 constexpr int kBarBytes = 512;
 constexpr int kChunk = kQuantThreads * 8;  // up: channels that the quantiser takes at a time
 // up: an item's activations, 16 tokens x 64 channels of bf16, rows 144 bytes apart
 constexpr int kActStride = 72;
 constexpr int kActBytes = kRows * kActStride * 2;
-static_assert(kSfCol + 16 * kMaxStages <= kTmemCols, "tensor memory");
+// Columns to allocate.  An allocation waits until the SM has them free, and the CTAs of a cluster wait
+// for one another, so whatever may be resident together (three CTAs of the down kernel from three
+// streams, one of each kernel) has to fit in the 512: 3 x 128, 128 + 256.  More than 6 stages are never
+// on an SM with a second CTA of as many: they take more than half of its shared memory.
+__device__ __forceinline__ int tmem_cols(int stages) { return kSfCol + 16 * stages <= 128 ? 128 : 256; }
+static_assert(kSfCol + 16 * kMaxStages <= 256, "tensor memory");
 
 // Shared memory of one CTA, byte offsets from a 1024-byte boundary.
 struct Layout {
@@ -335,7 +339,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
   const int stages = p.l.stages, bufs = p.l.bufs;
 
   if (warp == 1) {
-    tmem_alloc(tmem_holder, kTmemCols);
+    tmem_alloc(tmem_holder, tmem_cols(p.l.stages));
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
@@ -802,7 +806,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tmem_dealloc(tmem, tmem_cols(stages));
 }
 
 }  // namespace macaq
