@@ -40,6 +40,7 @@ constexpr int kMaxExperts = 512;
 constexpr int kMaxK = 8192;
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 2;
+constexpr int kPrefetch = 8;
 constexpr int kBCodeBytes = kRows * 128;  // codes of one K tile of a group
 constexpr int kBSfBytes = 512;            // its scales: two blocks of 16 rows x 16 bytes
 constexpr int kStageBytes = kTileCodeBytes + kTileSfBytes;
@@ -101,6 +102,12 @@ struct MoeParams {
   uint8_t* tables;       // the groups' tables, copied from the up kernel's first CTA (nullptr: the down
                          // kernel chooses for itself, while the up kernel runs)
   int S;                 // CTAs of a cluster (up: those that share the choosing)
+  // up: K tiles' weight images that a CTA has copied to L2, of its own linear while the experts are chosen
+  // and of the down kernel's, whose shape follows, behind its own: the memory works where it would wait
+  int early, ahead;
+  const uint8_t* Wq_next;
+  const uint8_t* Ws_next;
+  int NT_next, KT_next, S_next;
   int32_t* status;
   moe::Layout l;
 };
@@ -312,6 +319,12 @@ __device__ __forceinline__ int moe_groups(const MoeParams& p, uint8_t* smem, uin
   return grp_base;
 }
 
+// Lanes' part of copying a K tile's weight image to L2: an even one the codes, an odd one the scales.
+__device__ __forceinline__ void prefetch_image(const uint8_t* Wq, const uint8_t* Ws, size_t img, int lane) {
+  if (lane & 1) l2_prefetch(Ws + img * kTileSfBytes, kTileSfBytes);
+  else l2_prefetch(Wq + img * kTileCodeBytes, kTileCodeBytes);
+}
+
 // 80 registers: a CTA of each kernel on one SM is (512 + 256) x 80 of its 65536.
 template <bool kDown>
 __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) {
@@ -362,6 +375,15 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
   }
   if constexpr (!kDown) {
     if (p.S > 1) cluster_arrive_release();
+    if (warp == 0) {
+      // the weights that this CTA begins with if every expert is chosen by up to 16 tokens
+      const int first = static_cast<int>(static_cast<uint32_t>(p.rule.E * p.NT * blockIdx.x) / gridDim.x) * p.KT;
+      for (int i = lane; i < 2 * p.early; i += 32) {
+        const int kt = first + i / 2, item = kt / p.KT, e = item / p.NT;
+        if (e < p.rule.E)
+          prefetch_image(p.Wq, p.Ws, weight_image(e, item - e * p.NT, 0, p.NT / 2, p.KT) + 2 * (kt - item * p.KT), lane);
+      }
+    }
     pdl_wait();  // x and the logits may come from the kernel before
     // The down kernel may start: what it reads before its own wait is complete.  Warp 1 says so, after
     // its tensor memory is allocated: a CTA of the down kernel may take the rest of it and wait for us.
@@ -454,6 +476,19 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
           stage = 0;
           phase ^= 1;
         }
+      }
+    }
+    if constexpr (!kDown) {
+      // the down kernel's first items: of every share its first group, tile by tile, and so on
+      for (int i = lane; i < 2 * p.ahead; i += 32) {
+        int at = (i / 2) * shares + share;
+        const int kt = at % p.KT_next;
+        at /= p.KT_next;
+        const int tile = at % p.NT_next;
+        at /= p.NT_next;
+        const int r = at % p.S_next, g = G * r / p.S_next + at / p.S_next;
+        if (g < G * (r + 1) / p.S_next)
+          prefetch_image(p.Wq_next, p.Ws_next, weight_image(grp[g].y & 0xFFFF, tile, 0, p.NT_next / 2, p.KT_next) + 2 * kt, lane);
       }
     }
   } else if (warp == 1) {

@@ -145,6 +145,11 @@ __device__ __forceinline__ void bulk_g2s_hint_if(bool pred, void* dst, const voi
       : "memory");
 }
 
+// Copy global bytes (16-byte aligned, a multiple of 16) to L2; nothing waits for it.
+__device__ __forceinline__ void l2_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
