@@ -2827,9 +2827,11 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   down.S = std::min(8, groups);
   const int per_sm = 228 * 1024 / (down.l.bytes + 1024);  // the occupancy query counts one CTA per SM
   while (down.S > 1 && moe_clusters(dev, true, down.S, down.l.bytes) * per_sm < down.NT) --down.S;
-  // More tokens than a CTA has warps: a cluster shares the choosing.  Of 128 experts: 128 tokens 90 us alone, 84
-  // in pairs, 81 in fours (which leave 16 SMs out); 64 tokens 75, 71 and 69; 32 tokens 62, 60 and 60.
-  up.S = t > moe::kUpThreads / 16 ? 4 : t > moe::kUpThreads / 32 ? 2 : 1;
+  // A warp for every token: a cluster shares the choosing, up to 8 CTAs of 16 warps.  Of 128 experts: 128 tokens
+  // 90 us alone, 84 in pairs, 81 in fours, and 78.8 -> 77.4 from there in eights, which leave 28 SMs out; 64 tokens
+  // 75, 71 and 69 in fours; 32 tokens 62 and 60 in pairs.
+  up.S = 1;
+  while (up.S < 8 && up.S * (moe::kUpThreads / 32) < t) up.S *= 2;
   const int up_max = up.S == 1 ? sms : up.S * std::max(1, moe_clusters(dev, false, up.S, up.l.bytes));
   const int up_ctas = std::max(up.S, std::min(items, up_max) / up.S * up.S);
   // Images copied to L2 while the memory would wait.  8 of each (20 MB): one token 17.1 -> 16.0 us, 16 tokens
