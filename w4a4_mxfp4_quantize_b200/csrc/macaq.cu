@@ -2661,7 +2661,7 @@ static int route_ctas(int64_t T) {
 size_t macaq_route_workspace_bytes(int64_t T, int64_t E) {
   if (T <= 0 || T > INT32_MAX || E < 1 || E > kRouteMaxE) return 0;
   const int ctas = route_ctas(T);
-  return ctas > 1 ? static_cast<size_t>(ctas) * E * 4 : 0;
+  return ctas > 1 ? static_cast<size_t>(ctas) * hist_stride(static_cast<int>(E)) * 4 : 0;
 }
 
 int macaq_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t k, int score, int renorm,
