@@ -2825,7 +2825,9 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   // the largest cluster of which all fit at once (of 8, 15 do: at 2048 channels clusters of 7 take 112 SMs,
   // where 16 clusters of 8 would run one of them alone at the end and clusters of 4 take 64)
   down.S = std::min(8, groups);
-  const int per_sm = 228 * 1024 / (down.l.bytes + 1024);  // the occupancy query counts one CTA per SM
+  // (the occupancy query counts one CTA per SM.  Beside a CTA of the up kernel there is room for one only, and a late
+  // cluster starts when the up kernel ends; still, 4 tokens take 25.4 us so and 26.3 in clusters that all start early)
+  const int per_sm = 228 * 1024 / (down.l.bytes + 1024);
   while (down.S > 1 && moe_clusters(dev, true, down.S, down.l.bytes) * per_sm < down.NT) --down.S;
   // A warp for every token: a cluster shares the choosing, up to 8 CTAs of 16 warps.  Of 128 experts: 128 tokens
   // 90 us alone, 84 in pairs, 81 in fours, and 78.8 -> 77.4 from there in eights, which leave 28 SMs out; 64 tokens
