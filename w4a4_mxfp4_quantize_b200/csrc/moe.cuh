@@ -19,10 +19,10 @@
 // every CTA.  With few choices (T k <= 32) both kernels choose for themselves: a CTA of
 // each fits on an SM, and the down kernel, a programmatic dependent, streams its first
 // weight tiles while the up kernel still runs.  With more, clusters of the up kernel
-// share the choosing, its first CTA writes the groups' tables to the workspace, and the
-// weights that the down kernel begins with are copied to L2 meanwhile.  The activations
-// are quantised where they are made: in the down kernel every one of its N / 128 tiles
-// would do it again.
+// share the choosing and its first CTA writes the groups' tables to the workspace.  In
+// both cases the up kernel copies weights to L2 while it chooses, and behind its own the
+// down kernel's first.  The activations are quantised where they are made: in the down
+// kernel every one of its N / 128 tiles would do it again.
 //
 // Measured with 128 experts, 8 a token, H = 2048, I = 768: 1 token 16 us, 16 tokens 46,
 // 128 tokens 77.  Then all the experts' weights are read, 321 MB at 4.2 TB/s; while they
