@@ -15,17 +15,21 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import subprocess
 import sysconfig
 import threading
+import warnings
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 _LIB_PATH = os.path.join(_HERE, "libmacaq.so")
-_BINDING_PATH = os.path.join(_HERE, "_binding.so")
+# the compiled short way is good for one Python and one torch, so its name carries both
+_BINDING_PATH = os.path.join(_HERE, f"_binding.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 _SRC = os.path.join(_HERE, "csrc", "macaq.cu")
 _INCLUDE = os.path.join(_ROOT, "include")
 
@@ -64,7 +68,8 @@ def _older(path: str, sources) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libmacaq.so for sm_100a in-tree (nvcc cross-compiles without a GPU), and the
-    module with the short way to the calls around the linear (_binding.so, g++)."""
+    module with the short way to the calls around the linear (g++ and torch's headers; where
+    it cannot be compiled a RuntimeWarning says so, and the calls go through ctypes)."""
     if force or _older(_LIB_PATH, _sources((".cu", ".cuh"))):
         tmp = _LIB_PATH + f".tmp{os.getpid()}"
         cmd = ["nvcc", *NVCC_FLAGS, "-I" + _INCLUDE, "-o", tmp, _SRC]
@@ -73,17 +78,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.check_call(cmd)
         os.replace(tmp, _LIB_PATH)
     if force or _older(_BINDING_PATH, _sources((".cpp",))):
-        from torch.utils import cpp_extension
-
-        tmp = _BINDING_PATH + f".tmp{os.getpid()}"
-        include = [_INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
-        subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp,
-                               os.path.join(_HERE, "csrc", "binding.cpp"), *("-I" + d for d in include),
-                               *("-L" + d for d in cpp_extension.library_paths("cuda")), "-L" + _HERE,
-                               "-l:" + os.path.basename(_LIB_PATH), "-Wl,-rpath,$ORIGIN", "-ltorch_python", "-ltorch",
-                               "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
-        os.replace(tmp, _BINDING_PATH)
+        try:
+            _build_binding()
+        except (ImportError, OSError, subprocess.CalledProcessError) as e:
+            warnings.warn(f"{os.path.basename(_BINDING_PATH)} was not built: {e}", RuntimeWarning, stacklevel=2)
     return _LIB_PATH
+
+
+def _build_binding():
+    from torch.utils import cpp_extension
+
+    tmp = _BINDING_PATH + f".tmp{os.getpid()}"
+    include = [_INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp,
+                           os.path.join(_HERE, "csrc", "binding.cpp"), *("-I" + d for d in include),
+                           *("-L" + d for d in cpp_extension.library_paths("cuda")), "-L" + _HERE,
+                           "-l:" + os.path.basename(_LIB_PATH), "-Wl,-rpath,$ORIGIN", "-ltorch_python", "-ltorch",
+                           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, _BINDING_PATH)
 
 
 _lib = None
@@ -160,17 +172,24 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-# The compiled short way (csrc/binding.cpp): None where it was not built, and the calls
-# then go through ctypes alone.
+# The compiled short way (csrc/binding.cpp): None where it was not built or cannot be loaded,
+# and the calls then go through ctypes alone.
 _fast = None
 
 
 def _load_binding():
     global _fast
-    if os.path.exists(_BINDING_PATH):
-        from . import _binding
-
-        _fast = _binding
+    if not os.path.exists(_BINDING_PATH):
+        return
+    loader = importlib.machinery.ExtensionFileLoader(__name__ + "._binding", _BINDING_PATH)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"{os.path.basename(_BINDING_PATH)} was left out, it cannot be loaded: {e}", RuntimeWarning,
+                      stacklevel=3)
+        return
+    _fast = module
 
 
 def exported_symbols() -> list[str]:
