@@ -258,8 +258,8 @@ def _output(out, M: int, N: int, device):
 
 # ---------------------------------------------------------------------------
 # workspace: scratch for the quantise-once and grouped paths.  Callers may pass
-# their own (e.g. to capture calls in a CUDA graph); otherwise one buffer per
-# (device, stream) is kept and grown on demand.
+# their own (e.g. to capture calls in a CUDA graph, or from several threads on one
+# stream); otherwise one buffer per (device, stream) is kept and grown on demand.
 # ---------------------------------------------------------------------------
 _ws: dict = {}
 
@@ -728,16 +728,13 @@ def _place(stream, *ts):
 
 
 def _scratch(nbytes: int, dev: int, given: torch.Tensor | None):
-    """Workspace of a call on the current stream.  A captured call gets memory of its own
-    from the graph's pool: two graphs never share it, and the kept buffer may be regrown."""
+    """Workspace of a call on the current stream: the caller's, or memory of the call's own.
+    Threads that share a stream may queue the two kernels of their calls interleaved, and
+    two captured graphs may run at once, so no buffer is kept for the next call."""
     if nbytes == 0:
         return None
     if given is None:
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        buf = _ws.get((dev, _raw_stream(dev)))
-        if buf is not None and buf.numel() >= nbytes:
-            return buf
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return workspace(nbytes, torch.device("cuda", dev), None, given)
 
 
