@@ -385,6 +385,7 @@ __global__ void __maxnreg__(80) moe_kernel(const __grid_constant__ MoeParams p) 
     fence_mbar_init();
   }
   if constexpr (!kDown) {
+    __syncwarp();  // lane 0 of warp 0 was away
     if (p.S > 1) cluster_arrive_release();
     if (warp == 0) {
       // the weights that this CTA begins with if every expert is chosen by up to 16 tokens
