@@ -99,7 +99,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (gate.t != nullptr) {
     gate_type = element_type(gate);
     if (gate_type < 0 || gate.t->dim() != 2 || (a[4] != Py_None && !integer(a[4], per)) || per < 1 ||
-        !gate.is(gate.t->scalar_type(), dev, {(M + per - 1) / per, C}))
+        !gate.is(gate.t->scalar_type(), dev, {M > 0 ? (M - 1) / per + 1 : 0, C}))
       Py_RETURN_NONE;
   }
   Tensor out_h = empty(h.t->sizes(), h.t->scalar_type(), dev), out_n;

@@ -2605,7 +2605,7 @@ int macaq_block_norm(const void* h, int h_type, const uint16_t* y, const float* 
       (!y && (w_post != nullptr || gate != nullptr)))
     return MACAQ_ERR_NULL;
   const size_t hb = static_cast<size_t>(M) * C * element_bytes(h_type), yb = static_cast<size_t>(M) * C * 2;
-  const int64_t gates = gate != nullptr ? (M + rows_per_gate - 1) / rows_per_gate : 0;
+  const int64_t gates = gate != nullptr ? (M - 1) / rows_per_gate + 1 : 0;  // (any rows_per_gate: no overflow)
   const size_t gb = static_cast<size_t>(gates) * C * element_bytes(gate_type), wb = static_cast<size_t>(C) * 4;
   const struct { const void* p; size_t n; } in[] = {{h, hb}, {y, yb}, {w_post, wb}, {gate, gb}, {w_pre, wb}};
   for (const auto& i : in)
