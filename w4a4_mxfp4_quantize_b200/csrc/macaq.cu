@@ -42,6 +42,7 @@
 
 #include <cmath>
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <utility>
@@ -1671,11 +1672,13 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
+// What is asked once per device is kept in atomics: calls come from any thread.  Threads that
+// ask at the same time get the same answer and store it twice.
 struct DeviceState {
-  bool probed = false;
-  bool is_sm100 = false;
-  int sms = 0;
-  bool attrs_set = false;
+  std::atomic<bool> probed{false};  // the two below hold
+  std::atomic<bool> is_sm100{false};
+  std::atomic<int> sms{0};
+  std::atomic<bool> attrs_set{false};
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -1808,8 +1811,9 @@ int max_active_clusters_any(int bt_index, int S) {
 
 // Co-resident clusters per (BT, S), measured once per device.
 int active_clusters(int dev, int bt_index, int S) {
-  static int cache[kMaxDevices][4][9] = {};
-  int& v = cache[dev][bt_index][S];
+  static std::atomic<int> cache[kMaxDevices][4][9] = {};
+  std::atomic<int>& known = cache[dev][bt_index][S];
+  int v = known.load(std::memory_order_relaxed);
   if (v == 0) {
     switch (bt_index) {
       case 0: v = max_active_clusters<16>(S); break;
@@ -1818,6 +1822,7 @@ int active_clusters(int dev, int bt_index, int S) {
       default: v = max_active_clusters<128>(S);
     }
     if (v <= 0) v = -1;  // query failed: treat as one cluster per wave
+    known.store(v, std::memory_order_relaxed);
   }
   return v > 0 ? v : 1;
 }
@@ -2014,13 +2019,15 @@ int run_dense_two_kernel(const uint16_t* x, const float* D, const uint8_t* Wq, c
 static __device__ __align__(256) uint8_t g_noalloc_scratch[MACAQ_STATIC_SCRATCH_BYTES];
 
 int noalloc_scratch(int dev, uint8_t** out) {
-  static uint8_t* addr[kMaxDevices] = {};
-  if (addr[dev] == nullptr) {
+  static std::atomic<uint8_t*> addr[kMaxDevices] = {};
+  uint8_t* a = addr[dev];
+  if (a == nullptr) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr) return MACAQ_ERR_CUDA;
-    addr[dev] = static_cast<uint8_t*>(p);
+    a = static_cast<uint8_t*>(p);
+    addr[dev] = a;
   }
-  *out = addr[dev];
+  *out = a;
   return MACAQ_OK;
 }
 
@@ -2742,9 +2749,10 @@ static size_t moe_table_offset(int64_t T, int64_t k, int64_t I) {
 // Clusters of S CTAs of a kernel that the device holds at once, with `bytes` of shared memory each;
 // asked once per device, kernel, S and whole number of KiB.
 static int moe_clusters(int dev, bool down, int S, int bytes) {
-  static int16_t cache[kMaxDevices][2][8][228] = {};
+  static std::atomic<int16_t> cache[kMaxDevices][2][8][228] = {};
   const int kib = (bytes + 1023) / 1024;
-  int16_t& v = cache[dev][down ? 1 : 0][S - 1][kib - 1];
+  std::atomic<int16_t>& known = cache[dev][down ? 1 : 0][S - 1][kib - 1];
+  int v = known.load(std::memory_order_relaxed);
   if (v == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S);
@@ -2762,7 +2770,8 @@ static int moe_clusters(int dev, bool down, int S, int bytes) {
       cudaGetLastError();
       n = 1;
     }
-    v = static_cast<int16_t>(std::max(1, std::min(n, 32767)));
+    v = std::max(1, std::min(n, 32767));
+    known.store(static_cast<int16_t>(v), std::memory_order_relaxed);
   }
   return v;
 }
