@@ -54,7 +54,10 @@
 extern "C" {
 #endif
 
-#define MACAQ_ABI_VERSION 5  /* 5: the FP8-output calls */
+/* 5: the FP8-output calls.  The calls "around the linear" below and
+ * MACAQ_ERR_OPTION came later under the same number and changed no other call, so
+ * a library of version 5 may be without them: look a symbol up to tell. */
+#define MACAQ_ABI_VERSION 5
 
 #define MACAQ_OK 0
 #define MACAQ_ERR_NULL (-1)               /* a required pointer is NULL */
@@ -306,7 +309,9 @@ int macaq_block_norm(const void *h_dev, int h_type, const uint16_t *y_dev, const
 /* Routing: for each token the k experts of the largest logits (in falling order,
  * equal logits by the lowest index, a NaN as -infinity) and their weights
  *     w_j = scale * score(l_j)      or (renorm != 0) scale * score(l_j) / sum over the k
- * in FP32, and, sorted by expert, which rows the grouped linear would take:
+ * in FP32 with the hardware's exponential and division (a weight is within
+ * (2 (2 + span) + 16) 2^-22 of itself, span the largest |l - max|, for a sigmoid
+ * |l|), and, sorted by expert, which rows the grouped linear would take:
  *   logits_dev   [T, E] of logits_type;
  *   ids_dev      int32 [T, k];  weights_dev fp32 [T, k];
  *   counts_dev   int64 [E], the choices of each expert: a group_list of type 1
@@ -316,7 +321,8 @@ int macaq_block_norm(const void *h_dev, int h_type, const uint16_t *y_dev, const
  *                expert by token.  counts and order may both be NULL.
  * A logit of -infinity has weight zero, also in a token that has no other (its
  * ids are then the lowest experts); a sigmoid below 2^-126 is zero.  A NaN logit
- * makes a weight NaN where it is chosen or enters its sum.
+ * makes a weight NaN where it is chosen or enters its sum, and +infinity every
+ * softmax weight of its token.
  * Shapes: 0 <= T, T k <= 2^31 - 1; 1 <= E <= 1024 (MACAQ_ERR_TOO_MANY_GROUPS);
  * 1 <= k <= min(E, 32).  The workspace (macaq_route_workspace_bytes, 0 for a few
  * tokens) is used when counts is given; nothing in it has to start at zero. */
@@ -329,6 +335,8 @@ int macaq_moe_route(const void *logits_dev, int logits_type, int64_t T, int64_t 
  * [E, 2 I, K], per expert I gate rows followed by I up rows.  The images hold
  * them interleaved (row 2 c: gate row c, row 2 c + 1: up row c), so both halves
  * of a channel come out of one tile; sizes are macaq_weight_*_bytes(E, 2 I, K).
+ * macaq_grouped_mm takes the same images (more tokens than macaq_moe_mm does):
+ * its columns 2 c and 2 c + 1 are then gate and up of channel c.
  * Same checks and synchronisation as macaq_prepare_weights. */
 int macaq_prepare_gate_up(const float *W_dev, const float *D_dev, int64_t E, int64_t I, int64_t K, uint8_t *Wq_dev,
                           uint8_t *Ws_dev, void *stream);
@@ -352,7 +360,9 @@ int macaq_prepare_gate_up(const float *W_dev, const float *D_dev, int64_t E, int
  *   macaq_quantize_activations, then scales [T k, I / 32], row t k + j, rows of
  *   weight zero not written; then tables); nothing in it has to start at zero, and calls
  *   that share it must not run concurrently.
- *   The activation is evaluated with an FP32 exponential and division.
+ *   The activation is evaluated in FP32 with the hardware's exponential and
+ *   division: act(g) u is within (4 + 2 |z|) 2^-22 of itself before it is rounded
+ *   (z: g for SILU, 2 sqrt(2/pi) (g + 0.044715 g^3) for GELU_TANH).
  * Shapes: 0 <= T <= 128; 1 <= E <= 512; 1 <= k <= min(E, 16); H and I multiples
  * of 256 in [256, 8192]. */
 size_t macaq_moe_workspace_bytes(int64_t T, int64_t k, int64_t I);

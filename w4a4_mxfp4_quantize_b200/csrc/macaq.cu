@@ -2658,7 +2658,7 @@ static RouteRule route_rule(const void* logits, int logits_type, int64_t E, int6
   r.scale = scale;
   return r;
 }
-// CTAs of the routing kernels: one up to 4 runs of tokens (it needs no second kernel),
+// CTAs of the routing kernels: one for one run of tokens (it needs no second kernel),
 // then one per run up to kRouteCtas.
 static int route_ctas(int64_t T) {
   const int64_t runs = (T + kRouteRun - 1) / kRouteRun;
@@ -2831,8 +2831,8 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   // at most T k groups (and an expert's further ones): more CTAs than that would have nothing to do
   const int groups = moe::max_groups(t, kk, e);
   const int items = groups * up.NT;
-  // the largest cluster of which all fit at once (of 8, 15 do: at 2048 channels clusters of 7 take 112 SMs,
-  // where 16 clusters of 8 would run one of them alone at the end and clusters of 4 take 64)
+  // the largest cluster of which all fit at once: at 2048 channels, 16 clusters, that is 6 on the measured GPU
+  // (96 SMs; of 8, 15 fit, and the last would run alone at the end)
   down.S = std::min(8, groups);
   // (the occupancy query counts one CTA per SM.  Beside a CTA of the up kernel there is room for one only, and a late
   // cluster starts when the up kernel ends; still, 4 tokens take 25.4 us so and 26.3 in clusters that all start early)
@@ -2845,9 +2845,11 @@ int macaq_moe_mm(const uint16_t* x, const void* logits, int logits_type, const f
   while (up.S < 8 && up.S * (moe::kUpThreads / 32) < t) up.S *= 2;
   const int up_max = up.S == 1 ? sms : up.S * std::max(1, moe_clusters(dev, false, up.S, up.l.bytes));
   const int up_ctas = std::max(up.S, std::min(items, up_max) / up.S * up.S);
-  // Images copied to L2 while the memory would wait.  8 of each (20 MB): one token 17.1 -> 16.0 us, 16 tokens
-  // 48.7 -> 46.2, 128 tokens 80.7 -> 79.0.  24 early ones stand before the first copies that are needed (4 tokens
-  // 25 -> 29 us, 128 tokens 81); 16 ahead give 46.8 and 79.9.
+  // Images copied to L2 while the memory would wait, 8 of each (20 MB).  In a captured graph, with neither, early
+  // alone, ahead alone, both: one token 17.2, 16.6, 16.5, 16.4 us; 4 tokens 27.0, 26.5, 25.3, 25.8; 16 tokens 47.3,
+  // 46.5, 47.2, 46.2; 128 tokens 77.6, 77.6, 77.2, 77.1.  (Few choices leave most early images unused: at 4 tokens
+  // they cost 0.5 us beside the others.)  24 early ones stand before the first copies that are needed (4 tokens
+  // 25 -> 29 us); 16 ahead are 0.6 to 0.9 us slower.
   up.early = std::min(moe::kPrefetch, ceil_div(e * up.NT * up.KT, up_ctas));
   up.ahead = std::min(moe::kPrefetch, ceil_div(groups * down.NT * down.KT, up_ctas));
   up.Wq_next = Wq_down; up.Ws_next = Ws_down;
