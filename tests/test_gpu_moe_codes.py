@@ -95,3 +95,24 @@ def test_grouped_calls_on_the_interleaved_images():
     pairs = mq.grouped_mm(rows, d, *mq.prepare_gate_up(cuda(w_up), d), counts, 1, 2 * I)
     halves = mq.grouped_mm(rows, d, *mq.prepare_weights(cuda(w_up), d), counts, 1, 2 * I)
     assert torch.equal(pairs[:, 0::2], halves[:, :I]) and torch.equal(pairs[:, 1::2], halves[:, I:])
+
+
+def test_one_copy_of_the_weights_for_few_tokens_and_many():
+    # the layer's call, and routing with two grouped calls on the same images as it is written for more tokens
+    E, H, I, T, k = 16, 512, 512, 128, 4
+    w_up, w_down, d_up, d_down = narrow_layer(E, H, I, seed=11)
+    n = torch.from_numpy(narrow_tokens(T, H, seed=12).view(np.int16)).view(torch.bfloat16).cuda()
+    logits = cuda(np.random.default_rng(13).standard_normal((T, E)).astype(np.float32))
+    D_up, D_down = cuda(d_up), cuda(d_down)
+    up, down = mq.prepare_gate_up(cuda(w_up), D_up), mq.prepare_weights(cuda(w_down), D_down)
+    few = mq.moe_mm(n, logits, D_up, *up, D_down, *down, inner=I, k=k)
+    ids, weights, counts, order = mq.moe_route(logits, k)
+    token, order = order.long() // k, order.long()
+    u = mq.grouped_mm(n[token], D_up, *up, counts, group_list_type=1, N=2 * I)
+    a = (torch.nn.functional.silu(u[:, 0::2].float()) * u[:, 1::2].float()).bfloat16()
+    v = mq.grouped_mm(a, D_down, *down, counts, group_list_type=1, N=H)
+    many = torch.zeros_like(n, dtype=torch.float32).index_add_(0, token, v * weights.view(-1)[order][:, None])
+    # the grouped calls round g and u to bf16, so an activation moves by up to d = 2^-7 of itself and its four-bit
+    # code crosses a border with probability d / s, then moving by the grid's step s <= 1/2 of the value: a mean square
+    # of d s <= 2^-8, 2^-4 of the output, and the experts' outputs' own rounding
+    assert (few.float() - many).norm() / many.norm() < 2.0 ** -4 + 2.0 ** -8
